@@ -4,7 +4,10 @@ The compute lives in libkda_prefill.so (hand-written CUDA behind the C ABI of
 include/kda_prefill.h).  This package only marshals arguments: ``capi`` is
 the ctypes binding with the C entry points' names, ``prefill`` a convenience
 call that allocates outputs and the workspace with torch and launches on the
-current CUDA stream.
+current CUDA stream.  The operators that stand around the recurrence in a layer
+(include/kda_layer.h) are called the same way: ``conv_prefill`` / ``conv_decode``
+(short causal convolution), ``scan_prefill`` / ``scan_decode`` (selective state
+space scan) and ``rms_norm``.
 """
 from __future__ import annotations
 
@@ -16,7 +19,10 @@ from typing import Optional
 # any use of the CUDA path without the built library raises ImportError.
 _CAPI_NAMES = {"kda_prefill", "kda_prefill_describe", "kda_prefill_status",
                "kda_prefill_workspace_size", "kda_status_string", "kda_version",
-               "kda_workspace_init", "make_shape", "kda_decode", "make_decode_shape"}
+               "kda_workspace_init", "make_shape", "kda_decode", "make_decode_shape",
+               "kda_conv_prefill", "kda_conv_decode", "kda_scan_prefill", "kda_scan_decode",
+               "kda_rms_norm"}
+_LAYER_NAMES = {"conv_prefill", "conv_decode", "scan_prefill", "scan_decode", "rms_norm"}
 KDA_OK = 0
 KDA_VARIANT_AUTO, KDA_VARIANT_SPLIT, KDA_VARIANT_FUSED = 0, 1, 2
 KDA_VARIANT_HYBRID, KDA_VARIANT_TOKEN, KDA_VARIANT_STREAM = 3, 4, 5
@@ -30,12 +36,18 @@ def __getattr__(name):
         return importlib.import_module(".capi", __name__)
     if name in _CAPI_NAMES:
         return getattr(importlib.import_module(".capi", __name__), name)
+    if name in _LAYER_NAMES:
+        fn = getattr(importlib.import_module(".layer", __name__), name)
+        globals()[name] = fn   # found directly from the second use on
+        return fn
     raise AttributeError(name)
 
 __all__ = ["capi", "prefill", "decode", "Workspace", "KDAError", "kda_prefill",
            "kda_prefill_describe", "kda_prefill_status", "kda_prefill_workspace_size",
            "kda_status_string", "kda_version", "kda_workspace_init", "make_shape", "kda_decode",
-           "make_decode_shape"]
+           "make_decode_shape", "conv_prefill", "conv_decode", "scan_prefill", "scan_decode",
+           "rms_norm", "kda_conv_prefill", "kda_conv_decode", "kda_scan_prefill",
+           "kda_scan_decode", "kda_rms_norm"]
 
 
 class KDAError(RuntimeError):

@@ -15,9 +15,11 @@ ROOT = os.path.dirname(PKG)
 CSRC = os.path.join(PKG, "csrc")
 LIB = os.path.join(PKG, "libkda_prefill.so")
 SOURCES = ["kda_api.cu", "kda_schedule.cu", "kda_prepare.cu", "kda_recurrence.cu",
-           "kda_fused.cu", "kda_stream.cu", "kda_token.cu", "kda_noalloc.cu"]
+           "kda_fused.cu", "kda_stream.cu", "kda_token.cu", "kda_noalloc.cu",
+           "kda_layer_api.cu", "kda_conv.cu", "kda_scan.cu", "kda_norm.cu"]
 HEADERS = ["kda_common.cuh", "sm100_primitives.cuh", "kda_prepare.cuh", "kda_recurrence.cuh",
-           "kda_chain.cuh", "kda_token.cuh"]
+           "kda_chain.cuh", "kda_token.cuh", "kda_layer.cuh"]
+PUBLIC = ["kda_prefill.h", "kda_layer.h"]
 
 
 def nvcc_path() -> str:
@@ -29,7 +31,7 @@ def nvcc_path() -> str:
 
 def _inputs():
     files = [os.path.join(CSRC, f) for f in SOURCES + HEADERS]
-    files.append(os.path.join(ROOT, "include", "kda_prefill.h"))
+    files += [os.path.join(ROOT, "include", f) for f in PUBLIC]
     return files
 
 
@@ -45,7 +47,7 @@ def build(force: bool = False, verbose: bool = False) -> str:
         return LIB
     tmp = LIB + f".tmp{os.getpid()}"
     cmd = [nvcc_path(), "-gencode", "arch=compute_100a,code=sm_100a", "-O3", "-lineinfo",
-           "-std=c++17", "-Xcompiler", "-fPIC", "-shared", "-I", os.path.join(ROOT, "include"),
+           "-std=c++17", "--threads", "0", "-Xcompiler", "-fPIC", "-shared", "-I", os.path.join(ROOT, "include"),
            "-o", tmp] + [os.path.join(CSRC, f) for f in SOURCES]
     if verbose:
         cmd.insert(1, "-Xptxas=-v")

@@ -1,4 +1,5 @@
-"""ctypes binding of libkda_prefill.so (the C ABI of include/kda_prefill.h).
+"""ctypes binding of libkda_prefill.so (the C ABI of include/kda_prefill.h and of
+include/kda_layer.h).
 
 Argument marshalling only: every step of the prefill runs in the library's
 CUDA kernels.  The names match the C entry points.  There is no CPU fallback:
@@ -46,6 +47,14 @@ KDA_FLAG_VALIDATE = 1
 KDA_FLAG_TEST_FORCE_TIMEOUT = 2
 KDA_FLAG_CU_SEQLENS_I64 = 4
 
+# layer operators (kda_layer.h)
+KDA_DTYPE_BF16, KDA_DTYPE_F16, KDA_DTYPE_F32, KDA_DTYPE_E4M3 = 0, 1, 2, 3
+KDA_LAYER_CU_SEQLENS_I64 = 1
+KDA_CONV_SILU = 2
+KDA_LAYER_KEEP_STATE = 4
+KDA_SCAN_SOFTPLUS = 8
+KDA_NORM_GATE_SIGMOID = 1
+
 
 class kda_shape_t(ctypes.Structure):
     _fields_ = [("num_seqs", ctypes.c_int32), ("total_tokens", ctypes.c_int32),
@@ -67,6 +76,26 @@ class kda_options_t(ctypes.Structure):
     _fields_ = [("variant", ctypes.c_int32), ("flags", ctypes.c_uint32),
                 ("events", ctypes.c_void_p * 3), ("frontend", ctypes.POINTER(kda_frontend_t)),
                 ("reserved", ctypes.c_int32 * 2)]
+
+
+_I32, _I64 = ctypes.c_int32, ctypes.c_int64
+
+
+class kda_conv_shape_t(ctypes.Structure):
+    _fields_ = [(n, _I32) for n in ("num_seqs", "tokens", "channels", "width", "parts",
+                                    "pool_size", "dtype", "reserved")] + [("x_stride", _I64)]
+
+
+class kda_scan_shape_t(ctypes.Structure):
+    _fields_ = [(n, _I32) for n in ("num_seqs", "tokens", "channels", "state_size", "groups",
+                                    "pool_size", "dtype", "max_seqlen")] + \
+               [(n, _I64) for n in ("x_stride", "dt_stride", "z_stride", "b_stride", "c_stride")]
+
+
+class kda_norm_shape_t(ctypes.Structure):
+    _fields_ = [(n, _I32) for n in ("tokens", "heads", "width", "group", "dtype", "out_dtype")] + \
+               [(n, _I64) for n in ("x_stride", "residual_stride", "residual_out_stride",
+                                    "gate_stride")] + [("eps", ctypes.c_float), ("reserved", _I32)]
 
 
 def _load():
@@ -97,6 +126,16 @@ def _load():
     lib.kda_decode.argtypes = [P, P, P, P, P, ctypes.c_float, P, P,
                                ctypes.POINTER(kda_decode_shape_t), P, P, P, ctypes.c_uint32,
                                ctypes.POINTER(kda_frontend_t), P]
+    # the layer operators: pointers, one shape struct by address, flags, stream
+    U = ctypes.c_uint32
+    for name, args in {
+            "kda_conv_prefill": [P] * 7 + [ctypes.POINTER(kda_conv_shape_t), P, P, U, P],
+            "kda_conv_decode": [P] * 5 + [ctypes.POINTER(kda_conv_shape_t), P, P, P, U, P],
+            "kda_scan_prefill": [P] * 12 + [ctypes.POINTER(kda_scan_shape_t), P, P, U, P],
+            "kda_scan_decode": [P] * 10 + [ctypes.POINTER(kda_scan_shape_t), P, P, P, U, P],
+            "kda_rms_norm": [P] * 4 + [ctypes.POINTER(kda_norm_shape_t), P, P, P, U, P]}.items():
+        fn = getattr(lib, name)
+        fn.restype, fn.argtypes = ctypes.c_int, args
     return lib
 
 
@@ -178,3 +217,35 @@ def kda_decode(q, k, v, g, beta, scale, state, state_indices, shape, out, step_s
     return int(lib.kda_decode(q, k, v, g, beta, ctypes.c_float(scale), state, state_indices,
                               ctypes.byref(shape), out, step_states, device_status,
                               int(flags), fe, stream))
+
+
+# The layer operators (include/kda_layer.h): pointer arguments are integers (device
+# addresses) or None, shape is the operator's struct.
+def kda_conv_prefill(x, weight, bias, state, state_indices, has_state, cu_seqlens, shape, out,
+                     device_status, flags, stream) -> int:
+    return lib.kda_conv_prefill(x, weight, bias, state, state_indices, has_state, cu_seqlens,
+                                shape, out, device_status, flags, stream)
+
+
+def kda_conv_decode(x, weight, bias, state, state_indices, shape, out, step_states,
+                    device_status, flags, stream) -> int:
+    return lib.kda_conv_decode(x, weight, bias, state, state_indices, shape, out, step_states,
+                               device_status, flags, stream)
+
+
+def kda_scan_prefill(x, dt, A_log, B, C, D, z, dt_bias, state, state_indices, has_state,
+                     cu_seqlens, shape, out, device_status, flags, stream) -> int:
+    return lib.kda_scan_prefill(x, dt, A_log, B, C, D, z, dt_bias, state, state_indices,
+                                has_state, cu_seqlens, shape, out, device_status, flags, stream)
+
+
+def kda_scan_decode(x, dt, A_log, B, C, D, z, dt_bias, state, state_indices, shape, out,
+                    step_states, device_status, flags, stream) -> int:
+    return lib.kda_scan_decode(x, dt, A_log, B, C, D, z, dt_bias, state, state_indices, shape,
+                               out, step_states, device_status, flags, stream)
+
+
+def kda_rms_norm(x, weight, residual, gate, shape, out, residual_out, scales, flags,
+                 stream) -> int:
+    return lib.kda_rms_norm(x, weight, residual, gate, shape, out, residual_out, scales, flags,
+                            stream)
