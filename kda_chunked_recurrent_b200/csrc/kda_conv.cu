@@ -17,70 +17,101 @@
 //
 // Tokens.  One thread per kV channels of a sequence: state rows and new rows in, outputs
 // and the shifted state out.
+#include <type_traits>
+
 #include "kda_layer.cuh"
 
 namespace kda {
 namespace layer {
 namespace conv {
 
-constexpr int kStrip = 16;
+constexpr int kStrip = 8;
 
 template <typename T>
 struct Cfg {
   static constexpr int kV = 4;   // channels per thread: 8 bytes of a 16-bit row, 16 of FP32
 };
 
-template <typename T, int W>
+// kVec: every row, the weights and the outputs may be read and written 16 bytes at a time
+// (then a thread's channels lie in one part); else element by element.
+template <typename T, int W, bool kVec>
 struct Taps {
   static constexpr int kV = Cfg<T>::kV;
-  float w[kV][W];
-  float bias[kV];
+  float2 w[W][kV / 2];      // tap j of channel pairs
+  float2 bias[kV / 2];
 
   __device__ __forceinline__ void load(const ConvParams& p, int c0) {
+    float f[kV * W], g[kV];
+    if constexpr (kVec) {
+      Vec<F32, kV * W> wv;
+      wv.template load<true>(p.weight + static_cast<int64_t>(c0) * W);
+      wv.unpack(f);
+    }
     const int n = min(kV, p.C - c0);
 #pragma unroll
     for (int i = 0; i < kV; ++i) {
+      if constexpr (!kVec) {
 #pragma unroll
-      for (int j = 0; j < W; ++j)
-        w[i][j] = i < n ? __ldg(p.weight + static_cast<int64_t>(c0 + i) * W + j) : 0.f;
-      bias[i] = (p.bias != nullptr && i < n) ? __ldg(p.bias + c0 + i) : 0.f;
+        for (int j = 0; j < W; ++j)
+          f[i * W + j] = i < n ? p.weight[static_cast<int64_t>(c0 + i) * W + j] : 0.f;
+      }
+      g[i] = (p.bias != nullptr && i < n) ? p.bias[c0 + i] : 0.f;
+    }
+#pragma unroll
+    for (int i = 0; i < kV / 2; ++i) {
+#pragma unroll
+      for (int j = 0; j < W; ++j) w[j][i] = make_float2(f[2 * i * W + j], f[(2 * i + 1) * W + j]);
+      bias[i] = make_float2(g[2 * i], g[2 * i + 1]);
     }
   }
   // u: the W window rows, oldest first
   __device__ __forceinline__ void apply(const float (&u)[W][kV], bool act, float (&y)[kV]) const {
+    float2 a[kV / 2];
 #pragma unroll
-    for (int i = 0; i < kV; ++i) {
-      float a = bias[i];
+    for (int i = 0; i < kV / 2; ++i) {
+      a[i] = bias[i];
 #pragma unroll
-      for (int j = 0; j < W; ++j) a = fmaf(w[i][j], u[j][i], a);
-      y[i] = act ? silu(a) : a;
+      for (int j = 0; j < W; ++j)
+        a[i] = fma2<true>(w[j][i], make_float2(u[j][2 * i], u[j][2 * i + 1]), a[i]);
+    }
+    if (act) {
+#pragma unroll
+      for (int i = 0; i < kV / 2; ++i) a[i] = silu2(a[i]);
+    }
+#pragma unroll
+    for (int i = 0; i < kV / 2; ++i) {
+      y[2 * i] = a[i].x;
+      y[2 * i + 1] = a[i].y;
     }
   }
 };
 
-// Address of out row `row`, channel c0 (parts are contiguous blocks of all rows).
-template <typename T>
-__device__ __forceinline__ typename T::Raw* out_at(const ConvParams& p, int64_t row, int c) {
-  const int part = c / p.part_c;
-  return static_cast<typename T::Raw*>(p.out) +
-         (static_cast<int64_t>(part) * p.seq.rows + row) * p.part_c + (c - part * p.part_c);
-}
-
-// Store kV outputs; without the vector path a thread's channels may straddle two parts.
-template <typename T>
-__device__ __forceinline__ void put(const ConvParams& p, int64_t row, int c0,
-                                    const float (&y)[Cfg<T>::kV]) {
-  constexpr int kV = Cfg<T>::kV;
-  if (p.vec) {
-    Vec<T, kV> r;
-    r.pack(y);
-    r.store(out_at<T>(p, row, c0), true, kV);
-  } else {
-#pragma unroll
-    for (int i = 0; i < kV; ++i)
-      if (c0 + i < p.C) *out_at<T>(p, row, c0 + i) = T::from(y[i]);
+// Where a thread's channels go: parts are contiguous blocks of all rows.
+template <typename T, bool kVec>
+struct Out {
+  static constexpr int kV = Cfg<T>::kV;
+  using Raw = typename T::Raw;
+  Raw* base;   // channel c0 of row 0
+  const ConvParams& p;
+  int c0;
+  __device__ __forceinline__ Out(const ConvParams& p_, int c) : p(p_), c0(c) { base = at(c); }
+  __device__ __forceinline__ Raw* at(int c) const {
+    const int part = c / p.part_c;
+    return static_cast<Raw*>(p.out) + static_cast<int64_t>(part) * p.seq.rows * p.part_c +
+           (c - part * p.part_c);
   }
-}
+  __device__ __forceinline__ void put(int64_t row, const float (&y)[kV]) const {
+    if constexpr (kVec) {
+      Vec<T, kV> r;
+      r.pack(y);
+      r.template store<true>(base + row * p.part_c);
+    } else {
+#pragma unroll
+      for (int i = 0; i < kV; ++i)
+        if (c0 + i < p.C) at(c0 + i)[row * p.part_c] = T::from(y[i]);
+    }
+  }
+};
 
 // The largest n with start(n) <= t, by the whole warp: 32 probes a round.
 __device__ __forceinline__ int32_t find_seq(const Seqs& s, int32_t t) {
@@ -98,71 +129,83 @@ __device__ __forceinline__ int32_t find_seq(const Seqs& s, int32_t t) {
   return lo;
 }
 
-template <typename T, int W>
+template <typename T, int W, bool kVec>
 __device__ __forceinline__ void strips_body(const ConvParams& p, int group, int c0) {
   constexpr int kV = Cfg<T>::kV;
   using Raw = typename T::Raw;
-  const Raw* x = static_cast<const Raw*>(p.x) + c0;
   const bool on = c0 < p.C;
   const int count = p.C - c0;
-  const int64_t rows = p.seq.rows;
-  int64_t t0 = static_cast<int64_t>(group) * p.strips_per_cta * kStrip;
-  const int64_t t_end = min(rows, t0 + static_cast<int64_t>(p.strips_per_cta) * kStrip);
+  const int32_t rows = p.seq.rows;
+  int32_t t0 = group * p.strips_per_cta * kStrip;     // rows < 2^31 - 4096
+  const int32_t t_end = min(rows, t0 + p.strips_per_cta * kStrip);
+  const int64_t xs = p.x_stride;
+  // row t0 - (W - 1) + i is row i of px; it is only looked at where it exists
+  const Raw* px = static_cast<const Raw*>(p.x) + (static_cast<int64_t>(t0) - (W - 1)) * xs + c0;
   Vec<T, kV> r[W - 1 + kStrip];
-  // row t0 - (W - 1) + i in r[i]
-  auto fetch = [&](int from) {
+  const auto fetch = [&](auto from) {
+    if (on && t0 >= W - 1 && t0 + kStrip <= rows) {
 #pragma unroll
-    for (int i = 0; i < W - 1 + kStrip; ++i)
-      if (i >= from) {
-        const int64_t t = t0 - (W - 1) + i;
-        if (on && t >= 0 && t < rows) r[i].load(x + t * p.x_stride, p.vec, count);
+      for (int i = decltype(from)::value; i < W - 1 + kStrip; ++i) r[i].template load<kVec>(px + i * xs, count);
+    } else {
+#pragma unroll
+      for (int i = decltype(from)::value; i < W - 1 + kStrip; ++i) {
+        const int32_t t = t0 - (W - 1) + i;
+        if (on && t >= 0 && t < rows) r[i].template load<kVec>(px + i * xs, count);
         else r[i].clear();
       }
+    }
   };
-  fetch(0);
-  Taps<T, W> taps;
+  fetch(std::integral_constant<int, 0>());
+  Taps<T, W, kVec> taps;
   if (on) taps.load(p, c0);
-  int32_t n = find_seq(p.seq, static_cast<int32_t>(t0)), a, b;
+  const Out<T, kVec> out(p, on ? c0 : 0);
+  int32_t n = find_seq(p.seq, t0), a, b;
   p.seq.range(n, a, b);
   while (true) {
     float u[W][kV];
 #pragma unroll
     for (int j = 0; j < W - 1; ++j) r[j].unpack(u[j]);
-    const bool inside = a + W - 1 <= t0 && t0 + kStrip <= b;
-#pragma unroll
-    for (int i = 0; i < kStrip; ++i) {
-      const int32_t t = static_cast<int32_t>(t0) + i;
+    const auto row = [&](int i, bool live) {
       r[W - 1 + i].unpack(u[W - 1]);
-      bool live = true;
-      if (!inside) {
-        while (t >= b && n + 1 < p.seq.num) p.seq.range(++n, a, b);
-        live = t >= a + (W - 1) && t < b;
-      }
-      if (live && on) {
+      if (live) {
         float y[kV];
         taps.apply(u, p.silu, y);
-        put<T>(p, t, c0, y);
+        out.put(t0 + i, y);
       }
 #pragma unroll
       for (int j = 0; j + 1 < W; ++j)
 #pragma unroll
         for (int v = 0; v < kV; ++v) u[j][v] = u[j + 1][v];
+    };
+    if (a + W - 1 <= t0 && t0 + kStrip <= b) {
+      if (on) {
+#pragma unroll
+        for (int i = 0; i < kStrip; ++i) row(i, true);
+      }
+    } else {
+#pragma unroll
+      for (int i = 0; i < kStrip; ++i) {
+        const int32_t t = t0 + i;
+        while (t >= b && n + 1 < p.seq.num) p.seq.range(++n, a, b);
+        row(i, on && t >= a + (W - 1) && t < b);
+      }
     }
     if (t0 + kStrip >= t_end) break;
 #pragma unroll
     for (int j = 0; j < W - 1; ++j) r[j] = r[kStrip + j];
     t0 += kStrip;
-    fetch(W - 1);
+    px += kStrip * xs;
+    fetch(std::integral_constant<int, W - 1>());
   }
 }
 
 // The first W - 1 rows of sequence n and the state that it leaves.
-template <typename T, int W>
+template <typename T, int W, bool kVec>
 __device__ __forceinline__ void head_body(const ConvParams& p, int32_t n, int c0) {
   constexpr int kV = Cfg<T>::kV;
   using Raw = typename T::Raw;
   if (c0 >= p.C) return;
-  const int count = p.C - c0;
+  const int count = kVec ? kV : p.C - c0;
   int32_t a, b;
   p.seq.range(n, a, b);
   const int32_t len = b - a;
@@ -175,9 +218,9 @@ __device__ __forceinline__ void head_body(const ConvParams& p, int32_t n, int c0
   Vec<T, kV> past[W - 1], head[W - 1], tail[W - 1];
 #pragma unroll
   for (int j = 0; j < W - 1; ++j) {
-    if (old) past[j].load(st + static_cast<int64_t>(j) * p.C, p.vec, count);
+    if (old) past[j].template load<kVec>(st + static_cast<int64_t>(j) * p.C, count);
     else past[j].clear();
-    if (j < len) head[j].load(x + static_cast<int64_t>(a + j) * p.x_stride, p.vec, count);
+    if (j < len) head[j].template load<kVec>(x + static_cast<int64_t>(a + j) * p.x_stride, count);
     else head[j].clear();
   }
   if (slot >= 0) {
@@ -186,7 +229,7 @@ __device__ __forceinline__ void head_body(const ConvParams& p, int32_t n, int c0
     for (int j = 0; j < W - 1; ++j) {
       const int32_t r = len + j;
       if (r >= W - 1) {
-        tail[j].load(x + static_cast<int64_t>(a + r - (W - 1)) * p.x_stride, p.vec, count);
+        tail[j].template load<kVec>(x + static_cast<int64_t>(a + r - (W - 1)) * p.x_stride, count);
       } else {
 #pragma unroll
         for (int k = 0; k < W - 1; ++k)
@@ -194,8 +237,9 @@ __device__ __forceinline__ void head_body(const ConvParams& p, int32_t n, int c0
       }
     }
   }
-  Taps<T, W> taps;
+  Taps<T, W, kVec> taps;
   taps.load(p, c0);
+  const Out<T, kVec> out(p, c0);
   float u[2 * (W - 1)][kV];
 #pragma unroll
   for (int j = 0; j < W - 1; ++j) {
@@ -211,71 +255,87 @@ __device__ __forceinline__ void head_body(const ConvParams& p, int32_t n, int c0
 #pragma unroll
         for (int v = 0; v < kV; ++v) win[j][v] = u[i + j][v];
       taps.apply(win, p.silu, y);
-      put<T>(p, a + i, c0, y);
+      out.put(a + i, y);
     }
   if (slot >= 0) {
 #pragma unroll
     for (int j = 0; j < W - 1; ++j)
-      tail[j].store(st + static_cast<int64_t>(j) * p.C, p.vec, count);
+      tail[j].template store<kVec>(st + static_cast<int64_t>(j) * p.C, count);
   }
 }
 
 // Blocks [0, groups * cols) walk strips, blocks behind them take the sequence heads.
-template <typename T, int W>
+template <typename T, int W, bool kVec>
 __global__ void __launch_bounds__(256)
 kda_conv_prefill_kernel(const ConvParams p, int32_t cols, int32_t groups) {
   const int col = blockIdx.x % cols, i = blockIdx.x / cols;
   const int c0 = (col * blockDim.x + threadIdx.x) * Cfg<T>::kV;
-  if (i < groups) strips_body<T, W>(p, i, c0);
-  else head_body<T, W>(p, i - groups, c0);
+  if (i < groups) strips_body<T, W, kVec>(p, i, c0);
+  else head_body<T, W, kVec>(p, i - groups, c0);
 }
 
-template <typename T, int W>
+// kSeqs sequences at a time, so that their state rows and first new rows are all on their way
+// before any is used.
+template <typename T, int W, bool kVec, int kSeqs>
 __global__ void __launch_bounds__(256) kda_conv_decode_kernel(const ConvParams p, int32_t cols) {
   constexpr int kV = Cfg<T>::kV;
   using Raw = typename T::Raw;
   const int col = blockIdx.x % cols;
-  const int32_t n0 = static_cast<int32_t>(blockIdx.x / cols) * p.seqs_per_cta;
+  const int32_t n0 = static_cast<int32_t>(blockIdx.x / cols) * kSeqs;
   const int c0 = (col * blockDim.x + threadIdx.x) * kV;
   if (c0 >= p.C) return;
-  const int count = p.C - c0;
-  const int32_t T_new = p.seq.fixed_len, n_end = min(n0 + p.seqs_per_cta, p.seq.num);
-  Taps<T, W> taps;
-  taps.load(p, c0);
-  for (int32_t n = n0; n < n_end; ++n) {
-    const int32_t slot = state_slot(p.slot, n, p.pool, p.status, c0 == 0);
-    const int64_t row0 = static_cast<int64_t>(n) * T_new;
-    if (slot < 0) {   // a padding row: zero outputs
-      const float zero[kV] = {};
-      for (int32_t t = 0; t < T_new; ++t) put<T>(p, row0 + t, c0, zero);
-      continue;
-    }
-    const Raw* x = static_cast<const Raw*>(p.x) + row0 * p.x_stride + c0;
-    Raw* st = static_cast<Raw*>(p.state) + static_cast<int64_t>(slot) * (W - 1) * p.C + c0;
-    Vec<T, kV> win[W];
+  const int count = kVec ? kV : p.C - c0;
+  const int32_t T_new = p.seq.fixed_len;
+  const int64_t row_c = static_cast<int64_t>(p.C);
+  int32_t slot[kSeqs];
+  Vec<T, kV> win[kSeqs][W];
+#pragma unroll
+  for (int i = 0; i < kSeqs; ++i)
+    slot[i] = n0 + i < p.seq.num ? state_slot(p.slot, n0 + i, p.pool, p.status, c0 == 0) : -2;
+  const Raw* x = static_cast<const Raw*>(p.x) + c0;
+#pragma unroll
+  for (int i = 0; i < kSeqs; ++i) {
+    const Raw* st = static_cast<const Raw*>(p.state) + slot[i] * ((W - 1) * row_c) + c0;
 #pragma unroll
     for (int j = 0; j < W - 1; ++j)
-      win[j].load(st + static_cast<int64_t>(j) * p.C, p.vec, count);
+      if (slot[i] >= 0) win[i][j].template load<kVec>(st + j * row_c, count);
+      else win[i][j].clear();
+    if (slot[i] >= 0)
+      win[i][W - 1].template load<kVec>(x + static_cast<int64_t>(n0 + i) * T_new * p.x_stride, count);
+    else
+      win[i][W - 1].clear();
+  }
+  Taps<T, W, kVec> taps;
+  taps.load(p, c0);
+  const Out<T, kVec> out(p, c0);
+#pragma unroll
+  for (int i = 0; i < kSeqs; ++i) {
+    const int64_t row0 = static_cast<int64_t>(n0 + i) * T_new;
+    if (slot[i] == -2) break;
+    if (slot[i] < 0) {   // a padding row: zero outputs
+      const float zero[kV] = {};
+      for (int32_t t = 0; t < T_new; ++t) out.put(row0 + t, zero);
+      continue;
+    }
     for (int32_t t = 0; t < T_new; ++t) {
-      win[W - 1].load(x + t * p.x_stride, p.vec, count);
+      if (t > 0) win[i][W - 1].template load<kVec>(x + (row0 + t) * p.x_stride, count);
       float u[W][kV], y[kV];
 #pragma unroll
-      for (int j = 0; j < W; ++j) win[j].unpack(u[j]);
+      for (int j = 0; j < W; ++j) win[i][j].unpack(u[j]);
       taps.apply(u, p.silu, y);
-      put<T>(p, row0 + t, c0, y);
+      out.put(row0 + t, y);
 #pragma unroll
-      for (int j = 0; j < W - 1; ++j) win[j] = win[j + 1];
+      for (int j = 0; j < W - 1; ++j) win[i][j] = win[i][j + 1];
       if (p.steps != nullptr) {
-        Raw* sp = static_cast<Raw*>(p.steps) + (row0 + t) * (W - 1) * p.C + c0;
+        Raw* sp = static_cast<Raw*>(p.steps) + (row0 + t) * ((W - 1) * row_c) + c0;
 #pragma unroll
-        for (int j = 0; j < W - 1; ++j)
-          win[j].store(sp + static_cast<int64_t>(j) * p.C, p.vec, count);
+        for (int j = 0; j < W - 1; ++j) win[i][j].template store<kVec>(sp + j * row_c, count);
       }
     }
     if (!p.keep) {
+      Raw* st = static_cast<Raw*>(p.state) + slot[i] * ((W - 1) * row_c) + c0;
 #pragma unroll
-      for (int j = 0; j < W - 1; ++j)
-        win[j].store(st + static_cast<int64_t>(j) * p.C, p.vec, count);
+      for (int j = 0; j < W - 1; ++j) win[i][j].template store<kVec>(st + j * row_c, count);
     }
   }
 }
@@ -315,28 +375,30 @@ bool launch_prefill(ConvParams p, int W, int sms, cudaStream_t s) {
     kernel<<<static_cast<unsigned>(grid), sh.threads, 0, s>>>(p, sh.cols,
                                                               static_cast<int32_t>(groups));
   };
-  if (W == 2) go(kda_conv_prefill_kernel<T, 2>);
-  else if (W == 3) go(kda_conv_prefill_kernel<T, 3>);
-  else go(kda_conv_prefill_kernel<T, 4>);
+  if (W == 2) go(p.vec ? kda_conv_prefill_kernel<T, 2, true> : kda_conv_prefill_kernel<T, 2, false>);
+  else if (W == 3) go(p.vec ? kda_conv_prefill_kernel<T, 3, true> : kda_conv_prefill_kernel<T, 3, false>);
+  else go(p.vec ? kda_conv_prefill_kernel<T, 4, true> : kda_conv_prefill_kernel<T, 4, false>);
+  return true;
+}
+
+template <typename T, int W, int kSeqs>
+bool go_decode(const ConvParams& p, const Shape& sh, cudaStream_t s) {
+  const int64_t grid = static_cast<int64_t>((p.seq.num + kSeqs - 1) / kSeqs) * sh.cols;
+  if (grid > INT32_MAX) return false;
+  const auto kernel =
+      p.vec ? kda_conv_decode_kernel<T, W, true, kSeqs> : kda_conv_decode_kernel<T, W, false, kSeqs>;
+  kernel<<<static_cast<unsigned>(grid), sh.threads, 0, s>>>(p, sh.cols);
   return true;
 }
 
 template <typename T>
-bool launch_decode(ConvParams p, int W, int sms, cudaStream_t s) {
+bool launch_decode(const ConvParams& p, int W, int sms, cudaStream_t s) {
   const Shape sh = columns(p.C, Cfg<T>::kV);
-  // Sequences of a CTA share its weights; one CTA takes several once the batch fills the
-  // SMs many times over.
-  p.seqs_per_cta = static_cast<int64_t>(p.seq.num) * sh.cols >= 32LL * sms ? 4 : 1;
-  const int64_t grid = static_cast<int64_t>((p.seq.num + p.seqs_per_cta - 1) / p.seqs_per_cta) *
-                       sh.cols;
-  if (grid > INT32_MAX) return false;
-  const auto go = [&](auto kernel) {
-    kernel<<<static_cast<unsigned>(grid), sh.threads, 0, s>>>(p, sh.cols);
-  };
-  if (W == 2) go(kda_conv_decode_kernel<T, 2>);
-  else if (W == 3) go(kda_conv_decode_kernel<T, 3>);
-  else go(kda_conv_decode_kernel<T, 4>);
-  return true;
+  // Two sequences per thread once the batch fills the SMs without that.
+  const bool many = static_cast<int64_t>(p.seq.num) * sh.cols >= 8LL * sms;
+  if (W == 2) return many ? go_decode<T, 2, 2>(p, sh, s) : go_decode<T, 2, 1>(p, sh, s);
+  if (W == 3) return many ? go_decode<T, 3, 2>(p, sh, s) : go_decode<T, 3, 1>(p, sh, s);
+  return many ? go_decode<T, 4, 2>(p, sh, s) : go_decode<T, 4, 1>(p, sh, s);
 }
 
 }  // namespace conv

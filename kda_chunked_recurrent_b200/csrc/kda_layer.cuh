@@ -45,9 +45,9 @@ struct F32 {
   static __device__ __forceinline__ Raw from(float f) { return f; }
 };
 
-// n adjacent elements as 32-bit words, read and written whole where their address allows
-// (`vec`: a multiple of the vector's size, uniform over a launch) and element by element
-// up to `count` where not; elements past `count` read as 0 and are not written.
+// n adjacent elements as 32-bit words.  kVec: the address is a multiple of the vector's size
+// (at most 16 bytes) and all n elements are there, a property of the whole launch; else
+// element by element up to `count`: elements past it read as 0 and are not written.
 template <typename T, int n>
 struct Vec {
   static constexpr int kBytes = n * static_cast<int>(sizeof(typename T::Raw));
@@ -58,8 +58,9 @@ struct Vec {
 #pragma unroll
     for (int i = 0; i < kWords; ++i) w[i] = 0u;
   }
-  __device__ __forceinline__ void load(const typename T::Raw* p, bool vec, int count) {
-    if (vec && count >= n) {
+  template <bool kVec>
+  __device__ __forceinline__ void load(const typename T::Raw* p, int count = n) {
+    if constexpr (kVec) {
       if constexpr (kBytes % 16 == 0) {
 #pragma unroll
         for (int i = 0; i < kBytes / 16; ++i) {
@@ -78,20 +79,21 @@ struct Vec {
       } else {
         w[0] = *reinterpret_cast<const uint16_t*>(p);
       }
-      return;
-    }
-    clear();
+    } else {
+      clear();
 #pragma unroll
-    for (int i = 0; i < n; ++i)
-      if (i < count) {
-        if constexpr (sizeof(typename T::Raw) == 4)
-          w[i] = __float_as_uint(p[i]);
-        else
-          w[i / 2] |= static_cast<uint32_t>(p[i]) << (16 * (i % 2));
-      }
+      for (int i = 0; i < n; ++i)
+        if (i < count) {
+          if constexpr (sizeof(typename T::Raw) == 4)
+            w[i] = __float_as_uint(p[i]);
+          else
+            w[i / 2] |= static_cast<uint32_t>(p[i]) << (16 * (i % 2));
+        }
+    }
   }
-  __device__ __forceinline__ void store(typename T::Raw* p, bool vec, int count) const {
-    if (vec && count >= n) {
+  template <bool kVec>
+  __device__ __forceinline__ void store(typename T::Raw* p, int count = n) const {
+    if constexpr (kVec) {
       if constexpr (kBytes % 16 == 0) {
 #pragma unroll
         for (int i = 0; i < kBytes / 16; ++i)
@@ -104,16 +106,16 @@ struct Vec {
       } else {
         *reinterpret_cast<uint16_t*>(p) = static_cast<uint16_t>(w[0]);
       }
-      return;
-    }
+    } else {
 #pragma unroll
-    for (int i = 0; i < n; ++i)
-      if (i < count) {
-        if constexpr (sizeof(typename T::Raw) == 4)
-          p[i] = __uint_as_float(w[i]);
-        else
-          p[i] = static_cast<uint16_t>(w[i / 2] >> (16 * (i % 2)));
-      }
+      for (int i = 0; i < n; ++i)
+        if (i < count) {
+          if constexpr (sizeof(typename T::Raw) == 4)
+            p[i] = __uint_as_float(w[i]);
+          else
+            p[i] = static_cast<uint16_t>(w[i / 2] >> (16 * (i % 2)));
+        }
+    }
   }
   __device__ __forceinline__ void unpack(float (&f)[n]) const {
     if constexpr (sizeof(typename T::Raw) == 4) {
@@ -146,9 +148,18 @@ struct Vec {
 // ---- arithmetic ----------------------------------------------------------------------
 // 1 / (1 + e^-x); the reciprocal of an infinite denominator is 0, the limit
 __device__ __forceinline__ float sigmoid(float x) { return rcp_approx(1.f + ex2(-x * kLog2e)); }
-__device__ __forceinline__ float silu(float x) {
-  // for x below -88 the sigmoid is 0 while x may be -inf: the limit of the product is 0
-  return x < -88.f ? 0.f : x * sigmoid(x);
+__device__ __forceinline__ float2 sigmoid2(float2 x) {
+  const float2 t = mul2<true>(x, make_float2(-kLog2e, -kLog2e));
+  const float2 d = add2<true>(make_float2(ex2(t.x), ex2(t.y)), make_float2(1.f, 1.f));
+  return make_float2(rcp_approx(d.x), rcp_approx(d.y));
+}
+__device__ __forceinline__ float2 silu2(float2 x) { return mul2<true>(x, sigmoid2(x)); }
+
+// maximum that keeps a NaN
+__device__ __forceinline__ float max_nan(float a, float b) {
+  float r;
+  asm("max.NaN.f32 %0, %1, %2;" : "=f"(r) : "f"(a), "f"(b));
+  return r;
 }
 
 // ---- sequences -----------------------------------------------------------------------
@@ -203,7 +214,6 @@ struct ConvParams {
   int32_t silu, keep, vec;
   int32_t strips;           // prompts: row strips in all
   int32_t strips_per_cta;   // prompts: adjacent strips one CTA walks
-  int32_t seqs_per_cta;     // decode
 };
 
 struct ScanParams {
@@ -219,9 +229,6 @@ struct ScanParams {
   int64_t xs, ds, zs, bs, cs;   // row strides
   int32_t channels, size, groups, per_group, tiles_per_group, pool;
   int32_t softplus, keep;
-  int32_t vec;                  // rows of x, dt, z and out may be read in whole vectors
-  int32_t vec_bc;               // the same for B and C
-  int32_t seqs_per_cta;         // decode
 };
 
 struct NormParams {
@@ -232,8 +239,8 @@ struct NormParams {
   int64_t xs, rs, ros, gs;      // token strides
   int64_t rows;                 // tokens * heads
   int32_t heads, width, group, groups;
-  int32_t out8, sigmoid, vec, vec_w;
-  float eps;
+  int32_t out8, sigmoid, vec;
+  float eps, inv_width;
 };
 
 }  // namespace layer

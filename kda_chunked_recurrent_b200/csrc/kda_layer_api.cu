@@ -14,7 +14,7 @@ namespace layer {
 bool launch_conv_prefill(const ConvParams& p, int W, int dtype, int sms, cudaStream_t s);
 bool launch_conv_decode(const ConvParams& p, int W, int dtype, int sms, cudaStream_t s);
 bool launch_scan_prefill(const ScanParams& p, int dtype, int sms, cudaStream_t s);
-bool launch_scan_decode(const ScanParams& p, int dtype, int sms, cudaStream_t s);
+bool launch_scan_decode(const ScanParams& p, int dtype, cudaStream_t s);
 bool launch_norm(const NormParams& p, int dtype, cudaStream_t s);
 }  // namespace layer
 }  // namespace kda
@@ -161,7 +161,7 @@ kda_status_t conv_call(const void* x, const float* weight, const float* bias, vo
   p.silu = (flags & KDA_CONV_SILU) != 0;
   p.keep = (flags & KDA_LAYER_KEEP_STATE) != 0;
   p.vec = rows16(x, sh->x_stride, e) && rows16(state, C, e) && rows16(steps, C, e) &&
-          rows16(out, p.part_c, e) && C * e % 16 == 0;
+          rows16(out, p.part_c, e) && C * e % 16 == 0 && aligned(weight, 16);
   cudaStream_t s = static_cast<cudaStream_t>(stream);
   return launch(decode ? "kda_conv_decode" : "kda_conv_prefill", [&] {
     return decode ? launch_conv_decode(p, static_cast<int>(W), sh->dtype, sms, s)
@@ -247,7 +247,7 @@ kda_status_t scan_call(const void* x, const void* dt, const float* A_log, const 
   p.keep = (flags & KDA_LAYER_KEEP_STATE) != 0;
   cudaStream_t s = static_cast<cudaStream_t>(stream);
   return launch(decode ? "kda_scan_decode" : "kda_scan_prefill", [&] {
-    return decode ? launch_scan_decode(p, sh->dtype, sms, s)
+    return decode ? launch_scan_decode(p, sh->dtype, s)
                   : launch_scan_prefill(p, sh->dtype, sms, s);
   });
 }
@@ -362,9 +362,9 @@ kda_status_t kda_rms_norm(const void* x, const float* weight, const void* residu
   p.sigmoid = (flags & KDA_NORM_GATE_SIGMOID) != 0;
   p.vec = W % 8 == 0 && rows16(x, sh.x_stride, e) && rows16(residual, sh.residual_stride, e) &&
           rows16(residual_out, sh.residual_out_stride, e) && rows16(gate, sh.gate_stride, e) &&
-          aligned(out, out8 ? 8 : 16);
-  p.vec_w = aligned(weight, 16);
+          aligned(out, out8 ? 8 : 16) && aligned(weight, 16);
   p.eps = sh.eps;
+  p.inv_width = static_cast<float>(1.0 / static_cast<double>(W));
   cudaStream_t s = static_cast<cudaStream_t>(stream);
   return launch("kda_rms_norm", [&] { return launch_norm(p, sh.dtype, s); });
 }

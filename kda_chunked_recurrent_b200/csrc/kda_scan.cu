@@ -28,129 +28,217 @@ namespace layer {
 namespace scan {
 
 constexpr int kTB = 32;         // rows per block
-constexpr int kWarps = 4;       // scan warps; as many helper warps
-constexpr int kHelpers = 32 * kWarps;
-constexpr int kThreads = 2 * 32 * kWarps;
+constexpr int kHelpers = 128;   // helper threads
 constexpr int kU = 4;           // rows per step of the scan
+constexpr int kAhead = 6;       // blocks that a row is requested into L2 ahead of its turn
+
+__device__ __forceinline__ void prefetch_l2(const void* p) {
+  asm volatile("prefetch.global.L2 [%0];" ::"l"(p));
+}
 
 // log(1 + e^v) = max(v, 0) + log(1 + e), e = e^-|v| in (0, 1], with the logarithm from the
 // series of the inverse hyperbolic tangent, log(1 + e) = 2 atanh(s), s = e / (2 + e) <= 1/3,
 // which is relatively exact for a small e too (a step of 1e-3 is the usual case, and its
 // relative error is the state's): the first term left out is s^15 / 15, below 2^-27 of s.
-__device__ __forceinline__ float softplus(float v) {
-  const float e = ex2(-fabsf(v) * kLog2e);
-  const float s = e * rcp_approx(2.f + e), q = s * s;
-  float r = fmaf(q, 1.f / 13.f, 1.f / 11.f);
-  r = fmaf(q, r, 1.f / 9.f);
-  r = fmaf(q, r, 1.f / 7.f);
-  r = fmaf(q, r, 1.f / 5.f);
-  r = fmaf(q, r, 1.f / 3.f);
-  r = fmaf(q * s, r, s);
-  return fmaf(2.f, r, fmaxf(v, 0.f));
+__device__ __forceinline__ float2 splat(float v) { return make_float2(v, v); }
+__device__ __forceinline__ float2 softplus2(float2 v) {
+  const float2 e = make_float2(ex2(-fabsf(v.x) * kLog2e), ex2(-fabsf(v.y) * kLog2e));
+  const float2 t = add2<true>(e, splat(2.f));
+  const float2 s = mul2<true>(e, make_float2(rcp_approx(t.x), rcp_approx(t.y)));
+  const float2 q = mul2<true>(s, s);
+  float2 r = fma2<true>(q, splat(1.f / 13.f), splat(1.f / 11.f));
+  r = fma2<true>(q, r, splat(1.f / 9.f));
+  r = fma2<true>(q, r, splat(1.f / 7.f));
+  r = fma2<true>(q, r, splat(1.f / 5.f));
+  r = fma2<true>(q, r, splat(1.f / 3.f));
+  r = fma2<true>(mul2<true>(q, s), r, s);
+  return fma2<true>(splat(2.f), r, make_float2(fmaxf(v.x, 0.f), fmaxf(v.y, 0.f)));
 }
+__device__ __forceinline__ float softplus(float v) { return softplus2(make_float2(v, 0.f)).x; }
 
-// kNP state elements per channel (padded), kS of them per lane, kK channels per lane.
-template <int kNP_, int kS_, int kK_>
+// kNP state elements per channel (padded), kS of them per lane, kK channels per lane, kSW scan
+// warps; kPoly of the kU kS / 2 pairs of exponentials of a step and channel have one on the
+// FMA pipe.
+template <typename T, int kNP_, int kS_, int kK_, int kSW_, int kPoly_ = 0>
 struct Cfg {
-  static constexpr int kNP = kNP_, kS = kS_, kK = kK_;
+  static constexpr int kNP = kNP_, kS = kS_, kK = kK_, kSW = kSW_, kPoly = kPoly_;
   static constexpr int kL = kNP / kS;                   // lanes per channel
   static constexpr int kCW = 32 / kL;                   // channels side by side in a warp
-  static constexpr int kCH = kWarps * kCW * kK;         // channels per CTA
-  static constexpr int kE = kCH / 4;                    // channels per helper thread and row
+  static constexpr int kCH = kSW * kCW * kK;            // channels per CTA
+  static constexpr int kThreads = 32 * kSW + kHelpers;
+  // a helper thread has two rows of kE channels, and kQ elements of one row of B and of C
+  static constexpr int kE = kCH / 8, kQ = kNP / 4;
   // row pitch of the sums: a multiple of 4 floats that spreads the four rows which a warp
   // stores together over the banks
   static constexpr int kYP = kCH + (kCH >= 16 ? 8 : 4);
+  // 32-bit words of B (as many of C) that a lane reads per row, and of a row of both
+  static constexpr int kElem = sizeof(typename T::Raw);
+  static constexpr int kLW = kS * 2 * kElem / 4, kRW = kNP * 2 * kElem / 4;
   struct Stage {
-    float4 dd[kTB / 2][kCH];          // {d, d x} of an even row, then of the odd row
-    float B[kTB][kNP], C[kTB][kNP];
+    // {d, d} and {d x, d x} of an even row and the next.  Channel part kE + e is at place
+    // 8 e + part, here and in the sums: helper threads write, and scan lanes read, adjacent
+    // places, and a thread's channels stay adjacent in global memory.
+    float4 dd[kTB / 2][kCH];
+    // B and C in the rows' own type (half the bytes for 16 bits, and it is the reads from
+    // shared memory that bound the scan): per lane q its kS elements of B, then of C
+    uint32_t bc[kTB][kRW];
   };
+  static __device__ __forceinline__ int channel(int place) {
+    return (place % 8) * kE + place / 8;
+  }
   struct Smem {
     Stage st[2];
     float y[2][kTB][kYP];
   };
+  static_assert(kCH % 8 == 0 && kL >= 4, "eight helper parts; the exchange of four rows");
 };
 
+// 2^y on the FMA pipe: y = n + f, |f| <= 1/2, 2^f = 1 + f P(f) with P of degree 4 fitted for
+// the least relative error of 2^f (9e-8 before rounding); n goes into the exponent.  y is
+// taken to [-126, 128]: below, the decay is 2^-126; at 128 the result is infinite.
+__device__ __forceinline__ float ex2_fma(float y) {
+  y = fminf(fmaxf(y, -126.f), 128.f);
+  const float big = 12582912.f;   // 1.5 * 2^23: adding it rounds to an integer
+  const float t = y + big, f = y - (t - big);
+  float r = fmaf(f, 0.001326472731307149f, 0.009671512991189957f);
+  r = fmaf(f, r, 0.05550733581185341f);
+  r = fmaf(f, r, 0.24022242426872253f);
+  r = fmaf(f, r, 0.6931470036506653f);
+  r = fmaf(f, r, 1.f);
+  return __uint_as_float(__float_as_uint(r) + (__float_as_uint(t) << 23));
+}
+
+// The operands of kU rows for one lane, read from a stage.
 template <typename T, typename C>
-struct Helper {
-  using Raw = typename T::Raw;
-  static constexpr int kE = C::kE;
-  // B and C rows: kNP elements each; four threads a row take a quarter of both
-  static constexpr int kQ = C::kNP / 4;
-  Vec<T, kE> x[3], z[3];    // blocks in flight: loaded, being scanned, being written
-  Vec<T, kE> dt;
-  Vec<T, kQ> bq, cq;
-};
-
-// One block's scan by one warp.
-template <typename C>
-__device__ __forceinline__ void scan_block(const typename C::Stage& st, float (&yb)[kTB][C::kYP],
-                                           float (&h)[C::kK][C::kS], const float (&A)[C::kK][C::kS],
-                                           int ch0, int q, int nt) {
-  for (int t = 0; t < nt; t += kU) {
-    float sum[C::kK][kU];
-    float Bv[kU][C::kS], Cv[kU][C::kS];
+struct Rows {
+  static constexpr int kP = C::kS / 2 + (C::kS == 1);    // pairs of elements
+  uint32_t bc[kU][C::kLW];
+  float4 dd[C::kK][kU / 2];
+  __device__ __forceinline__ void load(const typename C::Stage& st, int t, int ch0, int q) {
 #pragma unroll
     for (int u = 0; u < kU; ++u) {
-      if constexpr (C::kS % 4 == 0) {
+      const uint32_t* w = &st.bc[t + u][q * C::kLW];
+      if constexpr (C::kLW % 4 == 0) {
 #pragma unroll
-        for (int i = 0; i < C::kS / 4; ++i) {
-          const float4 b = *reinterpret_cast<const float4*>(&st.B[t + u][q * C::kS + 4 * i]);
-          const float4 c = *reinterpret_cast<const float4*>(&st.C[t + u][q * C::kS + 4 * i]);
-          Bv[u][4 * i] = b.x; Bv[u][4 * i + 1] = b.y; Bv[u][4 * i + 2] = b.z; Bv[u][4 * i + 3] = b.w;
-          Cv[u][4 * i] = c.x; Cv[u][4 * i + 1] = c.y; Cv[u][4 * i + 2] = c.z; Cv[u][4 * i + 3] = c.w;
+        for (int i = 0; i < C::kLW / 4; ++i) {
+          const uint4 v = reinterpret_cast<const uint4*>(w)[i];
+          bc[u][4 * i] = v.x;
+          bc[u][4 * i + 1] = v.y;
+          bc[u][4 * i + 2] = v.z;
+          bc[u][4 * i + 3] = v.w;
         }
+      } else if constexpr (C::kLW == 2) {
+        const uint2 v = *reinterpret_cast<const uint2*>(w);
+        bc[u][0] = v.x;
+        bc[u][1] = v.y;
       } else {
-#pragma unroll
-        for (int i = 0; i < C::kS; ++i) {
-          Bv[u][i] = st.B[t + u][q * C::kS + i];
-          Cv[u][i] = st.C[t + u][q * C::kS + i];
-        }
+        bc[u][0] = *w;
       }
     }
 #pragma unroll
-    for (int k = 0; k < C::kK; ++k) {
-      const int ch = ch0 + k * C::kCW;
+    for (int k = 0; k < C::kK; ++k)
 #pragma unroll
-      for (int u2 = 0; u2 < kU; u2 += 2) {
-        const float4 dd = st.dd[(t + u2) / 2][ch];
-#pragma unroll
-        for (int o = 0; o < 2; ++o) {
-          const int u = u2 + o;
-          const float d = o ? dd.z : dd.x, dx = o ? dd.w : dd.y;
-          float acc = 0.f;
-#pragma unroll
-          for (int i = 0; i < C::kS; ++i) {
-            const float a = ex2(d * A[k][i]);
-            h[k][i] = fmaf(a, h[k][i], dx * Bv[u][i]);
-            acc = fmaf(Cv[u][i], h[k][i], acc);
-          }
-          sum[k][u] = acc;
-        }
-      }
+      for (int u = 0; u < kU; u += 2) dd[k][u / 2] = st.dd[(t + u) / 2][ch0 + k * C::kCW];
+  }
+  // elements 2 i and 2 i + 1 of B (of C), element 0 for kS == 1
+  __device__ __forceinline__ float2 pair(int u, int i, bool c) const {
+    if constexpr (C::kElem == 4) {
+      const uint32_t* w = &bc[u][c ? C::kS : 0];
+      return make_float2(__uint_as_float(w[2 * i]), C::kS == 1 ? 0.f : __uint_as_float(w[2 * i + 1]));
+    } else if constexpr (C::kS == 1) {
+      const float2 v = T::unpack2(bc[u][0]);
+      return make_float2(c ? v.y : v.x, 0.f);
+    } else {
+      return T::unpack2(bc[u][(c ? C::kLW / 2 : 0) + i]);
     }
-    // lanes q, q^1, q^2, q^3 exchange so that lane q holds row (q & 3); then the other lanes
+  }
+};
+
+// kU rows of the recurrence: h moves on, sum[k][u] is the lane's part of the read-out.
+template <typename T, typename C>
+__device__ __forceinline__ void step_rows(const Rows<T, C>& r, float (&h)[C::kK][C::kS],
+                                          const float (&A)[C::kK][C::kS], float (&sum)[C::kK][kU]) {
 #pragma unroll
-    for (int k = 0; k < C::kK; ++k) {
-      float v;
-      if constexpr (C::kL >= 4) {
-        const bool b0 = q & 1, b1 = q & 2;
-        const float s0 = b0 ? sum[k][0] : sum[k][1], k0 = b0 ? sum[k][1] : sum[k][0];
-        const float s1 = b0 ? sum[k][2] : sum[k][3], k1 = b0 ? sum[k][3] : sum[k][2];
-        const float p0 = k0 + __shfl_xor_sync(0xffffffffu, s0, 1);
-        const float p1 = k1 + __shfl_xor_sync(0xffffffffu, s1, 1);
-        v = (b1 ? p1 : p0) + __shfl_xor_sync(0xffffffffu, b1 ? p0 : p1, 2);
+  for (int k = 0; k < C::kK; ++k) {
 #pragma unroll
-        for (int o = 4; o < C::kL; o <<= 1) v += __shfl_xor_sync(0xffffffffu, v, o);
+    for (int u = 0; u < kU; ++u) {
+      const float4 dd = r.dd[k][u / 2];
+      const float d = u % 2 ? dd.y : dd.x, dx = u % 2 ? dd.w : dd.z;
+      if constexpr (C::kS == 1) {
+        h[k][0] = fmaf(ex2(d * A[k][0]), h[k][0], dx * r.pair(u, 0, false).x);
+        sum[k][u] = r.pair(u, 0, true).x * h[k][0];
+      } else {
+        float2 acc;
+#pragma unroll
+        for (int i = 0; i < C::kS; i += 2) {
+          const float2 y = mul2<true>(make_float2(d, d), make_float2(A[k][i], A[k][i + 1]));
+          const bool fma_pipe = ((u * (C::kS / 2) + i / 2) * C::kPoly) % (kU * C::kS / 2) <
+                                                    C::kPoly;
+          const float2 a = make_float2(ex2(y.x), fma_pipe ? ex2_fma(y.y) : ex2(y.y));
+          const float2 b = mul2<true>(make_float2(dx, dx), r.pair(u, i / 2, false));
+          const float2 n = fma2<true>(a, make_float2(h[k][i], h[k][i + 1]), b);
+          h[k][i] = n.x;
+          h[k][i + 1] = n.y;
+          const float2 c = r.pair(u, i / 2, true);
+          acc = i == 0 ? mul2<true>(c, n) : fma2<true>(c, n, acc);
+        }
+        sum[k][u] = acc.x + acc.y;
       }
-      if (q < 4) yb[t + q][ch0 + k * C::kCW] = v;
     }
   }
 }
 
+// Sums of kU rows over the kL lanes of a channel: in two exchanges the lanes q, q^1, q^2, q^3
+// are left with row q & 3 each, then the other lanes are added.
+template <typename C>
+__device__ __forceinline__ void reduce_rows(const float (&sum)[C::kK][kU],
+                                            float (&yb)[kTB][C::kYP], int t, int ch0, int q) {
+  const bool b0 = q & 1, b1 = q & 2;
+#pragma unroll
+  for (int k = 0; k < C::kK; ++k) {
+    const float p0 = (b0 ? sum[k][1] : sum[k][0]) +
+                     __shfl_xor_sync(0xffffffffu, b0 ? sum[k][0] : sum[k][1], 1);
+    const float p1 = (b0 ? sum[k][3] : sum[k][2]) +
+                     __shfl_xor_sync(0xffffffffu, b0 ? sum[k][2] : sum[k][3], 1);
+    float v = (b1 ? p1 : p0) + __shfl_xor_sync(0xffffffffu, b1 ? p0 : p1, 2);
+#pragma unroll
+    for (int o = 4; o < C::kL; o <<= 1) v += __shfl_xor_sync(0xffffffffu, v, o);
+    if (q < 4) yb[t + q][ch0 + k * C::kCW] = v;
+  }
+}
+
+// One block's scan by one warp, two groups of kU rows a turn: the next group's operands are
+// read while one is worked on, so that a scheduler with a single scan warp is kept busy.
+// Rows from nt on have d = 0 and B = C = 0 and change nothing.
 template <typename T, typename C>
-__global__ void __launch_bounds__(kThreads) kda_scan_prefill_kernel(const ScanParams p) {
+__device__ __forceinline__ void scan_block(const typename C::Stage& st, float (&yb)[kTB][C::kYP],
+                                           float (&h)[C::kK][C::kS], const float (&A)[C::kK][C::kS],
+                                           int ch0, int q, int nt) {
+  Rows<T, C> r0, r1;
+  float s0[C::kK][kU], s1[C::kK][kU];
+  r0.load(st, 0, ch0, q);
+  for (int t = 0; t < nt; t += 2 * kU) {
+    r1.load(st, t + kU, ch0, q);
+    step_rows<T, C>(r0, h, A, s0);
+    r0.load(st, (t + 2 * kU) % kTB, ch0, q);
+    reduce_rows<C>(s0, yb, t, ch0, q);
+    step_rows<T, C>(r1, h, A, s1);
+    reduce_rows<C>(s1, yb, t + kU, ch0, q);
+  }
+}
+
+// What a helper thread holds of a block: two rows of its channels, part of a row of B and C.
+template <typename T, typename C>
+struct Block {
+  Vec<T, C::kE> x[2], dt[2];
+  Vec<T, C::kQ> b, c;
+};
+
+// kVec: the rows' vectors may be moved whole (then a part is inside the tile or outside).
+template <typename T, typename C, bool kVec>
+__global__ void __launch_bounds__(C::kThreads) kda_scan_prefill_kernel(const ScanParams p) {
   using Raw = typename T::Raw;
-  static_assert(C::kL >= 4, "the exchange of four rows needs four lanes");
+  constexpr int kE = C::kE, kQ = C::kQ;
   extern __shared__ __align__(16) uint8_t smem_raw[];
   typename C::Smem& sm = *reinterpret_cast<typename C::Smem*>(smem_raw);
   const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
@@ -168,14 +256,14 @@ __global__ void __launch_bounds__(kThreads) kda_scan_prefill_kernel(const ScanPa
       p.state == nullptr ? -1 : state_slot(p.slot, n, p.pool, p.status, tile == 0 && tid == 0);
   if (len == 0 && slot < 0) return;
 
-  if (warp < kWarps) {
+  if (warp < C::kSW) {
     // ---- scan warps
-    const int q = lane % C::kL, ch0 = warp * (C::kCW * C::kK) + lane / C::kL;
+    const int q = lane % C::kL, ch0 = warp * (C::kCW * C::kK) + lane / C::kL;   // place
     float h[C::kK][C::kS], A[C::kK][C::kS];
     const bool old = slot >= 0 && (p.has == nullptr || p.has[n] != 0);
 #pragma unroll
     for (int k = 0; k < C::kK; ++k) {
-      const int ch = ch0 + k * C::kCW;
+      const int ch = C::channel(ch0 + k * C::kCW);
 #pragma unroll
       for (int i = 0; i < C::kS; ++i) {
         const int e = q * C::kS + i;
@@ -190,13 +278,13 @@ __global__ void __launch_bounds__(kThreads) kda_scan_prefill_kernel(const ScanPa
     }
     __syncthreads();
     for (int b = 0; b < nblk; ++b) {
-      scan_block<C>(sm.st[b & 1], sm.y[b & 1], h, A, ch0, q, min(kTB, len - b * kTB));
+      scan_block<T, C>(sm.st[b & 1], sm.y[b & 1], h, A, ch0, q, min(kTB, len - b * kTB));
       __syncthreads();
     }
     if (slot >= 0) {
 #pragma unroll
       for (int k = 0; k < C::kK; ++k) {
-        const int ch = ch0 + k * C::kCW;
+        const int ch = C::channel(ch0 + k * C::kCW);
 #pragma unroll
         for (int i = 0; i < C::kS; ++i) {
           const int e = q * C::kS + i;
@@ -209,252 +297,416 @@ __global__ void __launch_bounds__(kThreads) kda_scan_prefill_kernel(const ScanPa
     return;
   }
 
-  // ---- helper warps: thread -> row ht / 4 of a block, channels (ht % 4) kE .. + kE - 1
-  const int ht = tid - kHelpers, r = ht >> 2, part = ht & 3;
-  const int cl = part * C::kE, left = nch - cl;      // channels of this thread in the tile
-  const Raw* X = static_cast<const Raw*>(p.x) + cbase + cl;
-  const Raw* DT = static_cast<const Raw*>(p.dt) + cbase + cl;
-  const Raw* Z = static_cast<const Raw*>(p.z) + cbase + cl;
-  const Raw* Bp = static_cast<const Raw*>(p.B) + grp * p.size;
-  const Raw* Cp = static_cast<const Raw*>(p.Cm) + grp * p.size;
-  Raw* O = static_cast<Raw*>(p.out) + cbase + cl;
+  // ---- helper warps: rows 2 rp and 2 rp + 1 of a block, channels part kE .. + kE - 1; row br
+  // of B and C, elements quarter kQ .. + kQ - 1
+  const int ht = tid - 32 * C::kSW;
+  const int rp = ht >> 3, part = ht & 7, br = ht >> 2, quarter = ht & 3;
+  const int cl = part * kE, left = nch - cl;      // channels of this thread in the tile
+  const int left_bc = p.size - quarter * kQ;
   const bool gated = p.z != nullptr;
-  Helper<T, C> R;
-  float bias[C::kE], skip[C::kE];
+  const auto rows_at = [&](const void* base, int64_t stride, int64_t row, int64_t off) {
+    return static_cast<const Raw*>(base) + row * stride + off;
+  };
+  // rows of the block that is loaded next
+  const int64_t lrow = static_cast<int64_t>(row0) + 2 * rp, brow = static_cast<int64_t>(row0) + br;
+  const Raw* X = rows_at(p.x, p.xs, lrow, cbase + cl);
+  const Raw* DT = rows_at(p.dt, p.ds, lrow, cbase + cl);
+  const Raw* Bp = rows_at(p.B, p.bs, brow, static_cast<int64_t>(grp) * p.size + quarter * kQ);
+  const Raw* Cp = rows_at(p.Cm, p.cs, brow, static_cast<int64_t>(grp) * p.size + quarter * kQ);
+  // rows of the block that is written next
+  const Raw* FX = X;
+  const Raw* Z = gated ? rows_at(p.z, p.zs, lrow, cbase + cl) : nullptr;
+  Raw* O = static_cast<Raw*>(p.out) + lrow * p.channels + cbase + cl;
+  float2 bias[kE];
 #pragma unroll
-  for (int e = 0; e < C::kE; ++e) {
-    bias[e] = (p.dt_bias != nullptr && e < left) ? p.dt_bias[cbase + cl + e] : 0.f;
+  for (int e = 0; e < kE; ++e)
+    bias[e] = splat((p.dt_bias != nullptr && e < left) ? p.dt_bias[cbase + cl + e] : 0.f);
+  float skip[kE];
+#pragma unroll
+  for (int e = 0; e < kE; ++e)
     skip[e] = (p.D != nullptr && e < left) ? p.D[cbase + cl + e] : 0.f;
-  }
-  constexpr int kQ = Helper<T, C>::kQ;
-  auto load = [&](int b, Vec<T, C::kE>& x, Vec<T, C::kE>& z) {
-    const int64_t row = static_cast<int64_t>(row0) + b * kTB + r;
-    const bool on = row < row1;
-    if (on && left > 0) {
-      x.load(X + row * p.xs, p.vec, left);
-      R.dt.load(DT + row * p.ds, p.vec, left);
-      if (gated) z.load(Z + row * p.zs, p.vec, left);
-    } else {
-      x.clear();
-      R.dt.clear();
+
+  const auto load = [&](int b, Block<T, C>& k) {
+    const int rest = len - b * kTB;      // rows from the block's first on
+#pragma unroll
+    for (int o = 0; o < 2; ++o) {
+      if (left > 0 && 2 * rp + o < rest) {
+        k.x[o].template load<kVec>(X + o * p.xs, left);
+        k.dt[o].template load<kVec>(DT + o * p.ds, left);
+      } else {
+        k.x[o].clear();
+        k.dt[o].clear();
+      }
     }
-    const int n_bc = p.size - part * kQ;
-    if (on && n_bc > 0) {
-      R.bq.load(Bp + row * p.bs + part * kQ, p.vec_bc, n_bc);
-      R.cq.load(Cp + row * p.cs + part * kQ, p.vec_bc, n_bc);
+    if (left_bc > 0 && br < rest) {
+      k.b.template load<kVec>(Bp, left_bc);
+      k.c.template load<kVec>(Cp, left_bc);
     } else {
-      R.bq.clear();
-      R.cq.clear();
+      k.b.clear();
+      k.c.clear();
     }
+    X += kTB * p.xs;
+    DT += kTB * p.ds;
+    Bp += kTB * p.bs;
+    Cp += kTB * p.cs;
   };
   // rows past the sequence get d = 0: the state stays, their sums are not used
-  auto stage = [&](int b, const Vec<T, C::kE>& x) {
+  const auto stage = [&](int b, const Block<T, C>& k) {
     typename C::Stage& st = sm.st[b & 1];
-    const bool on = b * kTB + r < len;
-    float xf[C::kE], df[C::kE];
-    x.unpack(xf);
-    R.dt.unpack(df);
+    const int rest = len - b * kTB - 2 * rp;
+    float x0[kE], x1[kE], d0[kE], d1[kE];
+    k.x[0].unpack(x0);
+    k.x[1].unpack(x1);
+    k.dt[0].unpack(d0);
+    k.dt[1].unpack(d1);
 #pragma unroll
-    for (int e = 0; e < C::kE; ++e) {
-      float d = df[e] + bias[e];
-      if (p.softplus) d = softplus(d);
-      d = on && e < left ? d : 0.f;
-      float2* at = reinterpret_cast<float2*>(&st.dd[r >> 1][cl + e]) + (r & 1);
-      *at = make_float2(d, d * xf[e]);
+    for (int e = 0; e < kE; ++e) {
+      float2 d = add2<true>(make_float2(d0[e], d1[e]), bias[e]);
+      if (p.softplus) d = softplus2(d);
+      if (rest < 2) d = make_float2(rest > 0 ? d.x : 0.f, 0.f);
+      const float2 dx = mul2<true>(d, make_float2(x0[e], x1[e]));
+      st.dd[rp][8 * e + part] = make_float4(d.x, d.y, dx.x, dx.y);
     }
-    float f[kQ];
-    R.bq.unpack(f);
+    // the words of kQ elements: kS of B, kS of C, lane by lane
+    constexpr int kWords = kQ * 2 * C::kElem / 4, kHalf = C::kLW / 2;
+    uint32_t w[kWords];
+    if constexpr (kHalf == 0) {     // one element of 16 bits each: B low, C high
 #pragma unroll
-    for (int i = 0; i < kQ; ++i) st.B[r][part * kQ + i] = f[i];
-    R.cq.unpack(f);
+      for (int i = 0; i < kWords; ++i)
+        w[i] = __byte_perm(k.b.w[i / 2], k.c.w[i / 2], i % 2 ? 0x7632 : 0x5410);
+    } else {
 #pragma unroll
-    for (int i = 0; i < kQ; ++i) st.C[r][part * kQ + i] = f[i];
+      for (int i = 0; i < kWords / 2; ++i) {
+        w[i / kHalf * C::kLW + i % kHalf] = k.b.w[i];
+        w[i / kHalf * C::kLW + kHalf + i % kHalf] = k.c.w[i];
+      }
+    }
+    uint4* to = reinterpret_cast<uint4*>(&st.bc[br][quarter * kWords]);
+#pragma unroll
+    for (int i = 0; i < kWords / 4; ++i)
+      to[i] = make_uint4(w[4 * i], w[4 * i + 1], w[4 * i + 2], w[4 * i + 3]);
   };
-  auto finish = [&](int b, const Vec<T, C::kE>& x, const Vec<T, C::kE>& z) {
-    const int64_t row = static_cast<int64_t>(row0) + b * kTB + r;
-    if (row >= row1 || left <= 0) return;
-    float xf[C::kE], y[C::kE];
-    x.unpack(xf);
+  // x and z of the block to be written, loaded a while before
+  Vec<T, kE> fx[2], fz[2];
+  const auto finish_load = [&](int b) {
+    const int rest = len - b * kTB - 2 * rp;
 #pragma unroll
-    for (int e = 0; e < C::kE; ++e) y[e] = fmaf(skip[e], xf[e], sm.y[b & 1][r][cl + e]);
-    if (gated) {
-      float zf[C::kE];
-      z.unpack(zf);
+    for (int o = 0; o < 2; ++o)
+      if (left > 0 && o < rest) {
+        fx[o].template load<kVec>(FX + o * p.xs, left);
+        if (gated) fz[o].template load<kVec>(Z + o * p.zs, left);
+      }
+    FX += kTB * p.xs;
+    if (gated) Z += kTB * p.zs;
+  };
+  const auto finish = [&](int b) {
+    const int rest = len - b * kTB - 2 * rp;
+    if (left > 0) {
 #pragma unroll
-      for (int e = 0; e < C::kE; ++e) y[e] *= silu(zf[e]);
+      for (int o = 0; o < 2; ++o) {
+        if (o >= rest) break;
+        float xf[kE], zf[kE], y[kE];
+        fx[o].unpack(xf);
+#pragma unroll
+        for (int e = 0; e < kE; ++e) y[e] = fmaf(skip[e], xf[e], sm.y[b & 1][2 * rp + o][8 * e + part]);
+        if (gated) {
+          fz[o].unpack(zf);
+          if constexpr (kE == 1) {
+            y[0] *= zf[0] * sigmoid(zf[0]);
+          } else {
+#pragma unroll
+            for (int e = 0; e < kE; e += 2) {
+              const float2 g = silu2(make_float2(zf[e], zf[e + 1]));
+              y[e] *= g.x;
+              y[e + 1] *= g.y;
+            }
+          }
+        }
+        Vec<T, kE> v;
+        v.pack(y);
+        v.template store<kVec>(O + static_cast<int64_t>(o) * p.channels, left);
+      }
     }
-    Vec<T, C::kE> o;
-    o.pack(y);
-    o.store(O + row * p.channels, p.vec, left);
+    O += static_cast<int64_t>(kTB) * p.channels;
   };
 
+  // Rows come from HBM long before their turn: a thread asks for row br of x, dt, z, or of B
+  // and C, kAhead blocks ahead of the loads, which then find them in L2.
+  const Raw* ahead[2] = {nullptr, nullptr};
+  {
+    const int64_t row = brow + kAhead * kTB;
+    if (quarter == 0) ahead[0] = rows_at(p.x, p.xs, row, cbase);
+    if (quarter == 1) ahead[0] = rows_at(p.dt, p.ds, row, cbase);
+    if (quarter == 2 && gated) ahead[0] = rows_at(p.z, p.zs, row, cbase);
+    if (quarter == 3) {
+      ahead[0] = rows_at(p.B, p.bs, row, static_cast<int64_t>(grp) * p.size);
+      ahead[1] = rows_at(p.Cm, p.cs, row, static_cast<int64_t>(grp) * p.size);
+    }
+  }
+  const int64_t ahead_step =
+      kTB * (quarter == 0 ? p.xs : quarter == 1 ? p.ds : quarter == 2 ? p.zs : p.bs);
+  const int ahead_bytes = (quarter < 3 ? nch : p.size) * C::kElem;
+  const auto request = [&](int b) {      // the rows of block b + kAhead
+    if (ahead[0] != nullptr && (b + kAhead) * kTB + br < len) {
+      for (int o = 0; o < ahead_bytes; o += 128) {
+        prefetch_l2(reinterpret_cast<const char*>(ahead[0]) + o);
+        if (quarter == 3) prefetch_l2(reinterpret_cast<const char*>(ahead[1]) + o);
+      }
+    }
+    if (ahead[0] != nullptr) ahead[0] += ahead_step;
+    if (quarter == 3) ahead[1] += kTB * p.cs;
+  };
+
+  Block<T, C> k0, k1;
   if (nblk > 0) {
-    load(0, R.x[0], R.z[0]);
-    stage(0, R.x[0]);
-    if (nblk > 1) load(1, R.x[1], R.z[1]);
+    load(0, k0);
+    if (nblk > 1) load(1, k1);
+    stage(0, k0);
   }
   __syncthreads();
-  // before block b: stage b is ready, x[0], z[0] hold block b, x[1], z[1] block b + 1 (in
-  // flight), x[2], z[2] block b - 1
-  for (int b = 0; b < nblk; ++b) {
-    if (b > 0) finish(b - 1, R.x[2], R.z[2]);
-    if (b + 1 < nblk) stage(b + 1, R.x[1]);
-    R.x[2] = R.x[0];
-    R.z[2] = R.z[0];
-    R.x[0] = R.x[1];
-    R.z[0] = R.z[1];
-    if (b + 2 < nblk) load(b + 2, R.x[1], R.z[1]);
+  // Turn b, beside the scan of block b: block b + 2 is requested, block b + 1 (requested a
+  // turn ago) staged, block b - 1 written.
+  const auto turn = [&](int b, Block<T, C>& next, Block<T, C>& after) {
+    request(b);
+    if (b > 0) finish_load(b - 1);
+    if (b + 2 < nblk) load(b + 2, after);
+    if (b + 1 < nblk) stage(b + 1, next);
+    if (b > 0) finish(b - 1);
     __syncthreads();
+  };
+  for (int b = 0; b < nblk; b += 2) {
+    turn(b, k1, k0);
+    if (b + 1 < nblk) turn(b + 1, k0, k1);
   }
-  if (nblk > 0) finish(nblk - 1, R.x[2], R.z[2]);
+  if (nblk > 0) {
+    finish_load(nblk - 1);
+    finish(nblk - 1);
+  }
 }
 
-// ---- tokens: four elements per lane, kL lanes per channel
-template <typename T, int kL>
-__global__ void __launch_bounds__(256) kda_scan_decode_kernel(const ScanParams p) {
+// ---- tokens: four elements per lane, kL lanes per channel, four sequences at a time.
+// A lane's first duty is one of the four sequences: it alone loads dt, x and z there and takes
+// the softplus and the gate, and hands them to the other lanes of the channel; and it is left
+// with the sum of that sequence after the exchange.
+template <typename T, int kL, bool kVec>
+__global__ void __launch_bounds__(256, sizeof(typename T::Raw) == 4 ? 2 : 3)
+kda_scan_decode_kernel(const ScanParams p) {
   using Raw = typename T::Raw;
   constexpr int kCh = 256 / kL;     // channels per CTA
-  const int q = threadIdx.x % kL, cl = threadIdx.x / kL;
+  constexpr int kN = 4;             // sequences per CTA
+  const int q = threadIdx.x % kL, cl = threadIdx.x / kL, own = q & 3;
   const int tiles = p.tiles_per_group;                 // channel tiles (groups may share one)
   const int tile = blockIdx.x % tiles;
-  const int32_t n0 = static_cast<int32_t>(blockIdx.x / tiles) * p.seqs_per_cta;
-  const int32_t n1 = min(n0 + p.seqs_per_cta, p.seq.num);
+  const int32_t n0 = static_cast<int32_t>(blockIdx.x / tiles) * kN;
   const int ch = tile * kCh + cl;
   const bool on = ch < p.channels;
   const int c = on ? ch : p.channels - 1;              // idle threads follow the last channel
   const int e0 = 4 * q, count = on ? p.size - e0 : 0;  // state elements of this thread
-  const int grp = c / p.per_group;
-  float A[4];
+  const int32_t T_new = p.seq.fixed_len;
+  int32_t slot[kN];
 #pragma unroll
-  for (int i = 0; i < 4; ++i)
-    A[i] = i < count ? -expf(p.A_log[static_cast<int64_t>(c) * p.size + e0 + i]) * kLog2e : 0.f;
+  for (int s = 0; s < kN; ++s)
+    slot[s] = n0 + s < p.seq.num ? state_slot(p.slot, n0 + s, p.pool, p.status,
+                                              tile == 0 && threadIdx.x == 0)
+                                 : -1;
+  const int64_t state_at = static_cast<int64_t>(c) * p.size + e0;
+  const int64_t state_slot_size = static_cast<int64_t>(p.channels) * p.size;
+  Vec<F32, 4> sv[kN];
+#pragma unroll
+  for (int s = 0; s < kN; ++s) {
+    if (slot[s] >= 0 && count > 0)
+      sv[s].template load<kVec>(p.state + slot[s] * state_slot_size + state_at, count);
+    else
+      sv[s].clear();
+  }
+  // rows of token 0; token t is t strides on
+  const int64_t r_own = static_cast<int64_t>(n0 + own) * T_new;
+  const bool own_in = n0 + own < p.seq.num;
+  const bool own_live = own_in && (own == 0 ? slot[0] : own == 1 ? slot[1] : own == 2 ? slot[2]
+                                                                                      : slot[3]) >= 0;
+  const Raw* X = static_cast<const Raw*>(p.x) + r_own * p.xs + c;
+  const Raw* DT = static_cast<const Raw*>(p.dt) + r_own * p.ds + c;
+  const Raw* Z = static_cast<const Raw*>(p.z) + r_own * p.zs + c;
+  Raw* out = static_cast<Raw*>(p.out) + r_own * p.channels + c;
+  const int64_t bc_at = static_cast<int64_t>(c / p.per_group) * p.size + e0;
+  const Raw* Bp = static_cast<const Raw*>(p.B) + static_cast<int64_t>(n0) * T_new * p.bs + bc_at;
+  const Raw* Cp = static_cast<const Raw*>(p.Cm) + static_cast<int64_t>(n0) * T_new * p.cs + bc_at;
+  struct Row {
+    Raw x, dt, z;
+    Vec<T, 4> b[kN], c[kN];
+  };
+  const auto fetch = [&](Row& r, int32_t t) {
+    if (own_live) {
+      r.x = X[t * p.xs];
+      r.dt = DT[t * p.ds];
+      if (p.z != nullptr) r.z = Z[t * p.zs];
+    } else {
+      r.x = r.dt = r.z = Raw(0);
+    }
+#pragma unroll
+    for (int s = 0; s < kN; ++s) {
+      if (slot[s] >= 0 && count > 0) {
+        r.b[s].template load<kVec>(Bp + (static_cast<int64_t>(s) * T_new + t) * p.bs, count);
+        r.c[s].template load<kVec>(Cp + (static_cast<int64_t>(s) * T_new + t) * p.cs, count);
+      } else {
+        r.b[s].clear();
+        r.c[s].clear();
+      }
+    }
+  };
+  Row cur;
+  fetch(cur, 0);
+  float2 A[2];
+  {
+    Vec<F32, 4> av;
+    if (count > 0) av.template load<kVec>(p.A_log + state_at, count);
+    else av.clear();
+    float a[4];
+    av.unpack(a);
+#pragma unroll
+    for (int i = 0; i < 4; ++i) a[i] = i < count ? -expf(a[i]) * kLog2e : 0.f;
+    A[0] = make_float2(a[0], a[1]);
+    A[1] = make_float2(a[2], a[3]);
+  }
   const float bias = p.dt_bias != nullptr ? p.dt_bias[c] : 0.f;
   const float skip = p.D != nullptr ? p.D[c] : 0.f;
-  const bool vec_state = p.size % 4 == 0;
-  const int32_t T_new = p.seq.fixed_len;
-  for (int32_t n = n0; n < n1; ++n) {
-    const int32_t slot =
-        state_slot(p.slot, n, p.pool, p.status, tile == 0 && threadIdx.x == 0);
-    const int64_t r0 = static_cast<int64_t>(n) * T_new;
-    Raw* out = static_cast<Raw*>(p.out) + r0 * p.channels + c;
-    if (slot < 0) {   // a padding row: zero outputs
-      if (on && q == 0)
-        for (int32_t t = 0; t < T_new; ++t) out[static_cast<int64_t>(t) * p.channels] = T::from(0.f);
-      continue;
-    }
-    float* st = p.state + (static_cast<int64_t>(slot) * p.channels + c) * p.size + e0;
-    Vec<F32, 4> sv;
-    if (count > 0) sv.load(st, vec_state, count);
-    else sv.clear();
-    float h[4];
-    sv.unpack(h);
-    for (int32_t t = 0; t < T_new; ++t) {
-      const int64_t row = r0 + t;
-      const float x = T::to(static_cast<const Raw*>(p.x)[row * p.xs + c]);
-      float d = T::to(static_cast<const Raw*>(p.dt)[row * p.ds + c]) + bias;
-      const float z = p.z != nullptr ? T::to(static_cast<const Raw*>(p.z)[row * p.zs + c]) : 0.f;
-      Vec<T, 4> bv, cv;
-      if (count > 0) {
-        const int64_t at = static_cast<int64_t>(grp) * p.size + e0;
-        bv.load(static_cast<const Raw*>(p.B) + row * p.bs + at, p.vec_bc, count);
-        cv.load(static_cast<const Raw*>(p.Cm) + row * p.cs + at, p.vec_bc, count);
-      } else {
-        bv.clear();
-        cv.clear();
-      }
-      if (p.softplus) d = softplus(d);
-      const float dx = d * x;
-      float bf[4], cf[4], y = 0.f;
-      bv.unpack(bf);
-      cv.unpack(cf);
+  float2 h[kN][2];
 #pragma unroll
-      for (int i = 0; i < 4; ++i) {
-        h[i] = fmaf(ex2(d * A[i]), h[i], dx * bf[i]);
-        y = fmaf(cf[i], h[i], y);
-      }
+  for (int s = 0; s < kN; ++s) {
+    h[s][0] = make_float2(__uint_as_float(sv[s].w[0]), __uint_as_float(sv[s].w[1]));
+    h[s][1] = make_float2(__uint_as_float(sv[s].w[2]), __uint_as_float(sv[s].w[3]));
+  }
+  const auto pack_state = [&](int s) {
+    sv[s].w[0] = __float_as_uint(h[s][0].x);
+    sv[s].w[1] = __float_as_uint(h[s][0].y);
+    sv[s].w[2] = __float_as_uint(h[s][1].x);
+    sv[s].w[3] = __float_as_uint(h[s][1].y);
+  };
+  for (int32_t t = 0; t < T_new; ++t) {
+    const float x = T::to(cur.x);
+    float d = T::to(cur.dt) + bias;
+    if (p.softplus) d = softplus(d);
+    const float dx = d * x;
+    float part[kN];
 #pragma unroll
-      for (int o = 1; o < kL; o <<= 1) y += __shfl_xor_sync(0xffffffffu, y, o);
-      y = fmaf(skip, x, y);
-      if (p.z != nullptr) y *= silu(z);
-      if (on && q == 0) out[static_cast<int64_t>(t) * p.channels] = T::from(y);
-      if (p.steps != nullptr && count > 0) {
-        sv.pack(h);
-        sv.store(p.steps + (row * p.channels + c) * p.size + e0, vec_state, count);
+    for (int s = 0; s < kN; ++s) {
+      // from the lane of this channel whose duty is sequence s
+      const int src = (threadIdx.x & 28) | s;
+      const float ds = __shfl_sync(0xffffffffu, d, src), dxs = __shfl_sync(0xffffffffu, dx, src);
+      float bf[4], cf[4];
+      cur.b[s].unpack(bf);
+      cur.c[s].unpack(cf);
+      float2 acc;
+#pragma unroll
+      for (int i = 0; i < 2; ++i) {
+        const float2 e = mul2<true>(make_float2(ds, ds), A[i]);
+        h[s][i] = fma2<true>(make_float2(ex2(e.x), ex2(e.y)), h[s][i],
+                             mul2<true>(make_float2(dxs, dxs),
+                                        make_float2(bf[2 * i], bf[2 * i + 1])));
+        const float2 cv = make_float2(cf[2 * i], cf[2 * i + 1]);
+        acc = i == 0 ? mul2<true>(cv, h[s][0]) : fma2<true>(cv, h[s][1], acc);
       }
+      part[s] = acc.x + acc.y;
     }
-    if (!p.keep && count > 0) {
-      sv.pack(h);
-      sv.store(st, vec_state, count);
+    // four lanes exchange four sums, each keeps its own; then the other lanes of the channel
+    const bool b0 = own & 1, b1 = own & 2;
+    const float p0 = (b0 ? part[1] : part[0]) +
+                     __shfl_xor_sync(0xffffffffu, b0 ? part[0] : part[1], 1);
+    const float p1 = (b0 ? part[3] : part[2]) +
+                     __shfl_xor_sync(0xffffffffu, b0 ? part[2] : part[3], 1);
+    float y = (b1 ? p1 : p0) + __shfl_xor_sync(0xffffffffu, b1 ? p0 : p1, 2);
+#pragma unroll
+    for (int o = 4; o < kL; o <<= 1) y += __shfl_xor_sync(0xffffffffu, y, o);
+    y = fmaf(skip, x, y);
+    if (p.z != nullptr) {
+      const float z = T::to(cur.z);
+      y *= z * sigmoid(z);
     }
+    // a padding row's output is zero
+    if (on && q < 4 && own_in)
+      out[static_cast<int64_t>(t) * p.channels] = T::from(own_live ? y : 0.f);
+    if (t + 1 < T_new) fetch(cur, t + 1);
+    if (p.steps != nullptr && count > 0) {
+#pragma unroll
+      for (int s = 0; s < kN; ++s)
+        if (slot[s] >= 0) {
+          pack_state(s);
+          sv[s].template store<kVec>(
+              p.steps + (static_cast<int64_t>(n0 + s) * T_new + t) * state_slot_size + state_at,
+              count);
+        }
+    }
+  }
+  if (!p.keep && count > 0) {
+#pragma unroll
+    for (int s = 0; s < kN; ++s)
+      if (slot[s] >= 0) {
+        pack_state(s);
+        sv[s].template store<kVec>(p.state + slot[s] * state_slot_size + state_at, count);
+      }
   }
 }
 
 // ---- host side
+// Whether vectors of `bytes` (at most 16 at a time) may be taken from rows of q.
+bool whole(const void* q, int64_t stride_bytes, int bytes) {
+  const int a = bytes >= 16 ? 16 : bytes;
+  return q == nullptr || (reinterpret_cast<uintptr_t>(q) % a == 0 && stride_bytes % a == 0);
+}
+
 template <typename T, typename C>
 bool go_prefill(ScanParams p, cudaStream_t s) {
   p.tiles_per_group = (p.per_group + C::kCH - 1) / C::kCH;
-  constexpr int kBytes = C::kE * static_cast<int>(sizeof(typename T::Raw));
-  constexpr int kAlign = kBytes >= 16 ? 16 : kBytes;
-  constexpr int kBcBytes = C::kNP / 4 * static_cast<int>(sizeof(typename T::Raw));
-  constexpr int kBcAlign = kBcBytes >= 16 ? 16 : kBcBytes;
-  const auto ok = [](const void* q, int64_t stride, int align) {
-    return q == nullptr || (reinterpret_cast<uintptr_t>(q) % align == 0 &&
-                            stride * static_cast<int64_t>(sizeof(typename T::Raw)) % align == 0);
-  };
-  p.vec = ok(p.x, p.xs, kAlign) && ok(p.dt, p.ds, kAlign) && ok(p.z, p.zs, kAlign) &&
-          ok(p.out, p.channels, kAlign) && ok(nullptr, 0, 1) &&
-          (p.groups == 1 ||
-           p.per_group * static_cast<int64_t>(sizeof(typename T::Raw)) % kAlign == 0);
-  p.vec_bc = ok(p.B, p.bs, kBcAlign) && ok(p.Cm, p.cs, kBcAlign) &&
-             (p.groups == 1 ||
-              p.size * static_cast<int64_t>(sizeof(typename T::Raw)) % kBcAlign == 0);
+  constexpr int e = sizeof(typename T::Raw), kRow = C::kE * e, kBc = C::kQ * e;
+  const bool vec = whole(p.x, p.xs * e, kRow) && whole(p.dt, p.ds * e, kRow) &&
+                   whole(p.z, p.zs * e, kRow) &&
+                   whole(p.out, static_cast<int64_t>(p.channels) * e, kRow) &&
+                   p.per_group % C::kE == 0 && whole(p.B, p.bs * e, kBc) &&
+                   whole(p.Cm, p.cs * e, kBc) && p.size % C::kQ == 0;
   const int64_t grid = static_cast<int64_t>(p.seq.num) * p.groups * p.tiles_per_group;
   if (grid > INT32_MAX) return false;
   constexpr int kSmem = sizeof(typename C::Smem);
-  auto* kernel = kda_scan_prefill_kernel<T, C>;
+  const auto kernel =
+      vec ? kda_scan_prefill_kernel<T, C, true> : kda_scan_prefill_kernel<T, C, false>;
   if (kSmem > 48 * 1024 &&
       cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, kSmem) !=
           cudaSuccess)
     return false;
-  kernel<<<static_cast<unsigned>(grid), kThreads, kSmem, s>>>(p);
+  kernel<<<static_cast<unsigned>(grid), C::kThreads, kSmem, s>>>(p);
   return true;
 }
 
 template <typename T>
 bool launch_prefill(const ScanParams& p, int sms, cudaStream_t s) {
-  if (p.size > 64) return go_prefill<T, Cfg<128, 8, 1>>(p, s);
-  if (p.size > 32) return go_prefill<T, Cfg<64, 8, 1>>(p, s);
-  if (p.size > 16) return go_prefill<T, Cfg<32, 4, 1>>(p, s);
+  if (p.size > 64) return go_prefill<T, Cfg<T, 128, 8, 1, 4>>(p, s);
+  if (p.size > 32) return go_prefill<T, Cfg<T, 64, 8, 1, 4>>(p, s);
+  if (p.size > 16) return go_prefill<T, Cfg<T, 32, 4, 1, 4>>(p, s);
   const int64_t chains = static_cast<int64_t>(p.seq.num) * p.channels;
-  if (chains < 8LL * sms) return go_prefill<T, Cfg<16, 1, 1>>(p, s);
-  if (chains < 16LL * sms) return go_prefill<T, Cfg<16, 2, 1>>(p, s);
-  if (chains < 64LL * sms) return go_prefill<T, Cfg<16, 4, 1>>(p, s);
-  return go_prefill<T, Cfg<16, 4, 2>>(p, s);
+  if (chains < 8LL * sms) return go_prefill<T, Cfg<T, 16, 1, 1, 4>>(p, s);
+  if (chains < 16LL * sms) return go_prefill<T, Cfg<T, 16, 2, 1, 4>>(p, s);
+  if (chains < 64LL * sms) return go_prefill<T, Cfg<T, 16, 4, 1, 4>>(p, s);
+  return go_prefill<T, Cfg<T, 16, 4, 2, 4>>(p, s);
 }
 
 template <typename T, int kL>
-bool go_decode(ScanParams p, int sms, cudaStream_t s) {
-  constexpr int kCh = 256 / kL;
+bool go_decode(ScanParams p, cudaStream_t s) {
+  constexpr int kCh = 256 / kL, kN = 4, e = sizeof(typename T::Raw);
   p.tiles_per_group = (p.channels + kCh - 1) / kCh;
-  const auto ok = [](const void* q, int64_t stride) {
-    constexpr int a = 4 * static_cast<int>(sizeof(typename T::Raw));
-    return reinterpret_cast<uintptr_t>(q) % a == 0 && stride % 4 == 0;
-  };
-  p.vec_bc = ok(p.B, p.bs) && ok(p.Cm, p.cs) && (p.groups == 1 || p.size % 4 == 0);
-  p.seqs_per_cta = static_cast<int64_t>(p.seq.num) * p.tiles_per_group >= 32LL * sms ? 4 : 1;
-  const int64_t grid =
-      static_cast<int64_t>((p.seq.num + p.seqs_per_cta - 1) / p.seqs_per_cta) * p.tiles_per_group;
+  const bool vec = p.size % 4 == 0 && whole(p.B, p.bs * e, 4 * e) && whole(p.Cm, p.cs * e, 4 * e) &&
+                   whole(p.A_log, 0, 16);
+  const int64_t grid = static_cast<int64_t>((p.seq.num + kN - 1) / kN) * p.tiles_per_group;
   if (grid > INT32_MAX) return false;
-  kda_scan_decode_kernel<T, kL><<<static_cast<unsigned>(grid), 256, 0, s>>>(p);
+  const auto kernel = vec ? kda_scan_decode_kernel<T, kL, true> : kda_scan_decode_kernel<T, kL, false>;
+  kernel<<<static_cast<unsigned>(grid), 256, 0, s>>>(p);
   return true;
 }
 
 template <typename T>
-bool launch_decode(const ScanParams& p, int sms, cudaStream_t s) {
-  if (p.size > 64) return go_decode<T, 32>(p, sms, s);
-  if (p.size > 32) return go_decode<T, 16>(p, sms, s);
-  if (p.size > 16) return go_decode<T, 8>(p, sms, s);
-  return go_decode<T, 4>(p, sms, s);
+bool launch_decode(const ScanParams& p, cudaStream_t s) {
+  if (p.size > 64) return go_decode<T, 32>(p, s);
+  if (p.size > 32) return go_decode<T, 16>(p, s);
+  if (p.size > 16) return go_decode<T, 8>(p, s);
+  return go_decode<T, 4>(p, s);
 }
 
 }  // namespace scan
@@ -464,10 +716,10 @@ bool launch_scan_prefill(const ScanParams& p, int dtype, int sms, cudaStream_t s
   if (dtype == 1) return scan::launch_prefill<F16>(p, sms, s);
   return scan::launch_prefill<F32>(p, sms, s);
 }
-bool launch_scan_decode(const ScanParams& p, int dtype, int sms, cudaStream_t s) {
-  if (dtype == 0) return scan::launch_decode<Bf16>(p, sms, s);
-  if (dtype == 1) return scan::launch_decode<F16>(p, sms, s);
-  return scan::launch_decode<F32>(p, sms, s);
+bool launch_scan_decode(const ScanParams& p, int dtype, cudaStream_t s) {
+  if (dtype == 0) return scan::launch_decode<Bf16>(p, s);
+  if (dtype == 1) return scan::launch_decode<F16>(p, s);
+  return scan::launch_decode<F32>(p, s);
 }
 
 }  // namespace layer

@@ -18,7 +18,10 @@ from . import KDAError, capi
 
 _DTYPE = {torch.bfloat16: capi.KDA_DTYPE_BF16, torch.float16: capi.KDA_DTYPE_F16,
           torch.float32: capi.KDA_DTYPE_F32}
-_byref = ctypes.byref
+_byref, _lib = ctypes.byref, capi.lib
+# handle of a device's current stream, without making a Stream object where torch allows it
+_current_stream = getattr(torch._C, "_cuda_getCurrentRawStream", None) or (
+    lambda dev: torch.cuda.current_stream(dev).cuda_stream)
 
 
 def _fail(what):
@@ -29,6 +32,14 @@ def _ptr(t):
     return None if t is None else t.data_ptr()
 
 
+def _device(x):
+    """Index of the GPU that x is on."""
+    d = x.get_device()
+    if d < 0:
+        _fail(f"CUDA tensors expected, got one on {x.device}")
+    return d
+
+
 def _dtype(x, name):
     code = _DTYPE.get(x.dtype)
     if code is None:
@@ -36,89 +47,94 @@ def _dtype(x, name):
     return code
 
 
+# The checks of a call are on the path of every token: each looks at what it needs once and
+# returns what the launch takes (an address, a stride); the messages are made on failure only.
 def _like(name, t, dtype, shape, dev):
-    """A contiguous tensor of this type, shape and device, or None."""
+    """Address of a contiguous tensor of this type, shape and device; None for None."""
     if t is None:
-        return
-    if t.dtype != dtype or tuple(t.shape) != shape or t.device != dev or not t.is_contiguous():
-        _fail(f"{name}: a contiguous {dtype} tensor of shape {shape} on {dev} expected, got "
-              f"{t.dtype} {tuple(t.shape)} on {t.device}, strides {t.stride()}")
+        return None
+    if t.dtype is dtype and t.shape == shape and t.is_contiguous() and t.get_device() == dev:
+        return t.data_ptr()
+    _fail(f"{name}: a contiguous {dtype} tensor of shape {tuple(shape)} on GPU {dev} expected, "
+          f"got {t.dtype} {tuple(t.shape)} on {t.device}, strides {t.stride()}")
 
 
-def _rows(name, t, dtype, shape, dev, tail):
+def _vector(name, t, dtypes, n, dev):
+    """Address of n contiguous values of one of these types; None for None."""
+    if t is None:
+        return None
+    if t.dtype in dtypes and t.numel() == n and t.is_contiguous() and t.get_device() == dev:
+        return t.data_ptr()
+    _fail(f"{name}: {n} contiguous values of {dtypes} on GPU {dev} expected, got {t.numel()} of "
+          f"{t.dtype} on {t.device}")
+
+
+_INT32, _BYTES = (torch.int32,), (torch.bool, torch.uint8)
+
+
+def _rows(name, t, dtype, shape, dev, tail=1):
     """Elements between rows of a tensor [..., row] whose last ``tail`` dimensions are a
     contiguous row and whose leading dimensions step through rows at one stride."""
-    if t.dtype != dtype or tuple(t.shape) != shape or t.device != dev:
-        _fail(f"{name}: a {dtype} tensor of shape {shape} on {dev} expected, got {t.dtype} "
-              f"{tuple(t.shape)} on {t.device}")
-    st, n = t.stride(), 1
+    if t.dtype is not dtype or t.shape != shape or t.get_device() != dev:
+        _fail(f"{name}: a {dtype} tensor of shape {tuple(shape)} on GPU {dev} expected, got "
+              f"{t.dtype} {tuple(t.shape)} on {t.device}")
+    st = t.stride()
+    if tail == 1 and st[-1] == 1 and st[-2] >= shape[-1]:    # the usual layouts
+        if len(st) == 2 or st[0] == st[1] * shape[1]:
+            return st[-2]
+    n = 1
     for i in range(1, tail + 1):
         if shape[-i] != 1 and st[-i] != n:
             _fail(f"{name}: the elements of a row must be adjacent, strides {st}")
         n *= shape[-i]
-    lead, row = shape[:-tail], None
-    step = 1
-    for i in range(len(lead) - 1, -1, -1):
-        if lead[i] == 1:
+    row, step = None, 1
+    for i in range(len(st) - tail - 1, -1, -1):
+        if shape[i] == 1:
             continue
         if row is None:
-            row = st[i] // step if st[i] % step == 0 else -1
+            row = st[i]
         if st[i] != row * step:
             _fail(f"{name}: rows must lie at one distance, strides {st}")
-        step *= lead[i]
-    if row is None:
+        step *= shape[i]
+    if row is None or 0 in shape:
         return n
     if row < n:
-        if 0 in shape:
-            return n
         _fail(f"{name}: rows must not overlap, strides {st}")
     return row
 
 
-def _index(name, t, n, dev):
-    if t is not None and (t.dtype != torch.int32 or t.numel() != n or t.device != dev
-                          or not t.is_contiguous()):
-        _fail(f"{name}: {n} contiguous int32 values on {dev} expected")
-
-
 def _seqs(rows, cu_seqlens, num_seqs, state, state_indices, has_state, device_status, dev):
-    """Number of sequences and the flag of the offsets' type."""
-    flags = 0
+    """Number of sequences, the flag of the offsets' type, and the addresses of offsets,
+    slots, state marks and status word."""
+    flags, cu = 0, None
     if cu_seqlens is not None:
         N = cu_seqlens.numel() - 1
-        if (cu_seqlens.dtype not in (torch.int32, torch.int64) or N < 1
-                or cu_seqlens.device != dev or not cu_seqlens.is_contiguous()):
-            _fail(f"cu_seqlens: at least two contiguous int32 or int64 offsets on {dev} expected")
+        if cu_seqlens.dtype is torch.int64:
+            flags = capi.KDA_LAYER_CU_SEQLENS_I64
+        if N < 1:
+            _fail("cu_seqlens: at least two offsets expected")
+        cu = _vector("cu_seqlens", cu_seqlens, (torch.int32, torch.int64), N + 1, dev)
         if num_seqs is not None and num_seqs != N:
             _fail("num_seqs does not agree with cu_seqlens")
-        if cu_seqlens.dtype == torch.int64:
-            flags = capi.KDA_LAYER_CU_SEQLENS_I64
     else:
         N = 1 if num_seqs is None else int(num_seqs)
         if N < 1 or rows % N:
             _fail("without cu_seqlens the rows are num_seqs sequences of one length")
     if state is None and (state_indices is not None or has_state is not None):
         _fail("state_indices and has_state need a state")
-    _index("state_indices", state_indices, N, dev)
-    _index("device_status", device_status, 1, dev)
-    if has_state is not None and (has_state.dtype not in (torch.bool, torch.uint8)
-                                  or has_state.numel() != N or has_state.device != dev
-                                  or not has_state.is_contiguous()):
-        _fail(f"has_state: {N} contiguous bool or uint8 values on {dev} expected")
-    return N, flags
+    return (N, flags, cu, _vector("state_indices", state_indices, _INT32, N, dev),
+            _vector("has_state", has_state, _BYTES, N, dev),
+            _vector("device_status", device_status, _INT32, 1, dev))
 
 
 def _call(fn, where, dev, stream, *args):
     """Launch on the tensors' device: its current stream unless one is given."""
-    if dev.type != "cuda":
-        _fail(f"{where}: CUDA tensors expected, got {dev}")
-    if torch.cuda.current_device() == dev.index:
-        s = torch.cuda.current_stream(dev) if stream is None else stream
-        rc = fn(*args, s.cuda_stream)
+    s = _current_stream(dev) if stream is None else stream.cuda_stream
+    if torch.cuda.current_device() == dev:
+        rc = fn(*args, s)
     else:
         with torch.cuda.device(dev):
-            s = torch.cuda.current_stream(dev) if stream is None else stream
-            rc = fn(*args, s.cuda_stream)
+            rc = fn(*args, s)
     if rc != capi.KDA_OK:
         raise KDAError(rc, where)
 
@@ -127,9 +143,8 @@ def _conv_weight(weight, bias, C, dev):
     if weight.dim() != 2:
         _fail("weight: [channels, width] expected")
     W = weight.shape[1]
-    _like("weight", weight, torch.float32, (C, W), dev)
-    _like("bias", bias, torch.float32, (C,), dev)
-    return W
+    return (W, _like("weight", weight, torch.float32, (C, W), dev),
+            _like("bias", bias, torch.float32, (C,), dev))
 
 
 def _parts_shape(lead, C, parts):
@@ -153,24 +168,20 @@ def conv_prefill(x, weight, *, bias=None, state=None, state_indices=None, has_st
     """
     if x.dim() != 2:
         _fail("x: [T, C] expected")
-    dev, (T, C) = x.device, x.shape
+    (T, C), t, dev = x.shape, x.dtype, _device(x)
     code = _dtype(x, "x")
-    W = _conv_weight(weight, bias, C, dev)
-    N, flags = _seqs(T, cu_seqlens, num_seqs, state, state_indices, has_state, device_status, dev)
-    P = 0
-    if state is not None:
-        P = state.shape[0]
-        _like("state", state, x.dtype, (P, W - 1, C), dev)
+    W, pw, pb = _conv_weight(weight, bias, C, dev)
+    N, flags, pcu, pslot, phas, pstatus = _seqs(T, cu_seqlens, num_seqs, state, state_indices,
+                                                has_state, device_status, dev)
+    P = 0 if state is None else state.shape[0]
+    pstate = _like("state", state, t, (P, W - 1, C), dev)
     oshape = _parts_shape((T,), C, parts)
     if out is None:
-        out = torch.empty(oshape, dtype=x.dtype, device=dev)
-    else:
-        _like("out", out, x.dtype, oshape, dev)
-    shape = capi.kda_conv_shape_t(N, T, C, W, parts, P, code, 0,
-                                  _rows("x", x, x.dtype, (T, C), dev, 1))
-    _call(capi.kda_conv_prefill, "kda_conv_prefill", dev, stream, x.data_ptr(),
-          weight.data_ptr(), _ptr(bias), _ptr(state), _ptr(state_indices), _ptr(has_state),
-          _ptr(cu_seqlens), _byref(shape), out.data_ptr(), _ptr(device_status),
+        out = x.new_empty(oshape)
+    pout = _like("out", out, t, oshape, dev)
+    shape = capi.kda_conv_shape_t(N, T, C, W, parts, P, code, 0, _rows("x", x, t, (T, C), dev))
+    _call(_lib.kda_conv_prefill, "kda_conv_prefill", dev, stream, x.data_ptr(), pw, pb, pstate,
+          pslot, phas, pcu, _byref(shape), pout, pstatus,
           flags | (capi.KDA_CONV_SILU if silu else 0))
     return out
 
@@ -188,52 +199,47 @@ def conv_decode(x, weight, state, *, bias=None, state_indices=None, parts: int =
     """
     if x.dim() != 3:
         _fail("x: [N, T, C] expected")
-    dev, (N, T, C) = x.device, x.shape
+    (N, T, C), t, dev = x.shape, x.dtype, _device(x)
     code = _dtype(x, "x")
-    W = _conv_weight(weight, bias, C, dev)
+    W, pw, pb = _conv_weight(weight, bias, C, dev)
     P = state.shape[0]
-    _like("state", state, x.dtype, (P, W - 1, C), dev)
-    _index("state_indices", state_indices, N, dev)
-    _index("device_status", device_status, 1, dev)
+    pstate = _like("state", state, t, (P, W - 1, C), dev)
+    pslot = _vector("state_indices", state_indices, _INT32, N, dev)
+    pstatus = _vector("device_status", device_status, _INT32, 1, dev)
     oshape = _parts_shape((N, T), C, parts)
     if out is None:
-        out = torch.empty(oshape, dtype=x.dtype, device=dev)
-    else:
-        _like("out", out, x.dtype, oshape, dev)
+        out = x.new_empty(oshape)
+    pout = _like("out", out, t, oshape, dev)
     if step_states is None and return_step_states:
-        step_states = torch.empty(N, T, W - 1, C, dtype=x.dtype, device=dev)
-    elif step_states is not None:
-        _like("step_states", step_states, x.dtype, (N, T, W - 1, C), dev)
-    shape = capi.kda_conv_shape_t(N, T, C, W, parts, P, code, 0,
-                                  _rows("x", x, x.dtype, (N, T, C), dev, 1))
-    _call(capi.kda_conv_decode, "kda_conv_decode", dev, stream, x.data_ptr(), weight.data_ptr(),
-          _ptr(bias), state.data_ptr(), _ptr(state_indices), _byref(shape), out.data_ptr(),
-          _ptr(step_states), _ptr(device_status),
+        step_states = x.new_empty((N, T, W - 1, C))
+    psteps = _like("step_states", step_states, t, (N, T, W - 1, C), dev)
+    shape = capi.kda_conv_shape_t(N, T, C, W, parts, P, code, 0, _rows("x", x, t, (N, T, C), dev))
+    _call(_lib.kda_conv_decode, "kda_conv_decode", dev, stream, x.data_ptr(), pw, pb, pstate,
+          pslot, _byref(shape), pout, psteps, pstatus,
           (capi.KDA_CONV_SILU if silu else 0) | (capi.KDA_LAYER_KEEP_STATE if keep_state else 0))
     return out, step_states
 
 
-def _scan_args(x, dt, A_log, B, C, D, z, dt_bias, state, lead):
-    """Check the operands that both forms share; the shape struct without its sequences."""
-    dev, ch = x.device, x.shape[-1]
+def _scan_args(x, dt, A_log, B, C, D, z, dt_bias, state, rows, dev):
+    """Check the operands that both forms share: their addresses in the entry points' order
+    and the shape struct without its sequences.  rows: the shape of x."""
+    t, ch = x.dtype, rows[-1]
     code = _dtype(x, "x")
-    if A_log.dim() != 2 or B.dim() != len(lead) + 2:
+    if A_log.dim() != 2 or B.dim() != len(rows) + 1:
         _fail("A_log: [D, N] and B, C: [..., G, N] expected")
     size, groups = A_log.shape[1], B.shape[-2]
-    _like("A_log", A_log, torch.float32, (ch, size), dev)
-    _like("D", D, torch.float32, (ch,), dev)
-    _like("dt_bias", dt_bias, torch.float32, (ch,), dev)
-    P = 0
-    if state is not None:
-        P = state.shape[0]
-        _like("state", state, torch.float32, (P, ch, size), dev)
-    rows, bc = lead + (ch,), lead + (groups, size)
+    P = 0 if state is None else state.shape[0]
+    bc = (*rows[:-1], groups, size)
     shape = capi.kda_scan_shape_t(
-        0, 0, ch, size, groups, P, code, 0, _rows("x", x, x.dtype, rows, dev, 1),
-        _rows("dt", dt, x.dtype, rows, dev, 1),
-        0 if z is None else _rows("z", z, x.dtype, rows, dev, 1),
-        _rows("B", B, x.dtype, bc, dev, 2), _rows("C", C, x.dtype, bc, dev, 2))
-    return shape
+        0, 0, ch, size, groups, P, code, 0, _rows("x", x, t, rows, dev),
+        _rows("dt", dt, t, rows, dev), 0 if z is None else _rows("z", z, t, rows, dev),
+        _rows("B", B, t, bc, dev, 2), _rows("C", C, t, bc, dev, 2))
+    f32 = torch.float32
+    ptrs = (x.data_ptr(), dt.data_ptr(), _like("A_log", A_log, f32, (ch, size), dev),
+            B.data_ptr(), C.data_ptr(), _like("D", D, f32, (ch,), dev), _ptr(z),
+            _like("dt_bias", dt_bias, f32, (ch,), dev),
+            _like("state", state, f32, (P, ch, size), dev))
+    return ptrs, shape
 
 
 def scan_prefill(x, dt, A_log, B, C, *, D=None, z=None, dt_bias=None, state=None,
@@ -252,19 +258,16 @@ def scan_prefill(x, dt, A_log, B, C, *, D=None, z=None, dt_bias=None, state=None
     """
     if x.dim() != 2:
         _fail("x: [T, D] expected")
-    dev, (T, ch) = x.device, x.shape
-    N, flags = _seqs(T, cu_seqlens, num_seqs, state, state_indices, has_state, device_status, dev)
-    shape = _scan_args(x, dt, A_log, B, C, D, z, dt_bias, state, (T,))
-    shape.num_seqs, shape.tokens, shape.max_seqlen = N, T, max_seqlen
+    rows, dev = x.shape, _device(x)
+    N, flags, pcu, pslot, phas, pstatus = _seqs(rows[0], cu_seqlens, num_seqs, state,
+                                                state_indices, has_state, device_status, dev)
+    ptrs, shape = _scan_args(x, dt, A_log, B, C, D, z, dt_bias, state, rows, dev)
+    shape.num_seqs, shape.tokens, shape.max_seqlen = N, rows[0], max_seqlen
     if out is None:
-        out = torch.empty(T, ch, dtype=x.dtype, device=dev)
-    else:
-        _like("out", out, x.dtype, (T, ch), dev)
-    _call(capi.kda_scan_prefill, "kda_scan_prefill", dev, stream, x.data_ptr(), dt.data_ptr(),
-          A_log.data_ptr(), B.data_ptr(), C.data_ptr(), _ptr(D), _ptr(z), _ptr(dt_bias),
-          _ptr(state), _ptr(state_indices), _ptr(has_state), _ptr(cu_seqlens), _byref(shape),
-          out.data_ptr(), _ptr(device_status),
-          flags | (capi.KDA_SCAN_SOFTPLUS if softplus else 0))
+        out = x.new_empty(rows)
+    pout = _like("out", out, x.dtype, rows, dev)
+    _call(_lib.kda_scan_prefill, "kda_scan_prefill", dev, stream, *ptrs, pslot, phas, pcu,
+          _byref(shape), pout, pstatus, flags | (capi.KDA_SCAN_SOFTPLUS if softplus else 0))
     return out
 
 
@@ -281,25 +284,20 @@ def scan_decode(x, dt, A_log, B, C, state, *, D=None, z=None, dt_bias=None, stat
     """
     if x.dim() != 3:
         _fail("x: [N, T, D] expected")
-    dev, (N, T, ch) = x.device, x.shape
-    shape = _scan_args(x, dt, A_log, B, C, D, z, dt_bias, state, (N, T))
+    rows, dev = x.shape, _device(x)
+    N, T, ch = rows
+    ptrs, shape = _scan_args(x, dt, A_log, B, C, D, z, dt_bias, state, rows, dev)
     shape.num_seqs, shape.tokens = N, T
-    _index("state_indices", state_indices, N, dev)
-    _index("device_status", device_status, 1, dev)
+    pslot = _vector("state_indices", state_indices, _INT32, N, dev)
+    pstatus = _vector("device_status", device_status, _INT32, 1, dev)
     if out is None:
-        out = torch.empty(N, T, ch, dtype=x.dtype, device=dev)
-    else:
-        _like("out", out, x.dtype, (N, T, ch), dev)
-    size = shape.state_size
+        out = x.new_empty(rows)
+    pout = _like("out", out, x.dtype, rows, dev)
     if step_states is None and return_step_states:
-        step_states = torch.empty(N, T, ch, size, dtype=torch.float32, device=dev)
-    elif step_states is not None:
-        _like("step_states", step_states, torch.float32, (N, T, ch, size), dev)
-    _call(capi.kda_scan_decode, "kda_scan_decode", dev, stream, x.data_ptr(), dt.data_ptr(),
-          A_log.data_ptr(), B.data_ptr(), C.data_ptr(), _ptr(D), _ptr(z), _ptr(dt_bias),
-          state.data_ptr(), _ptr(state_indices), _byref(shape), out.data_ptr(),
-          _ptr(step_states), _ptr(device_status),
-          (capi.KDA_SCAN_SOFTPLUS if softplus else 0)
+        step_states = state.new_empty((N, T, ch, shape.state_size))
+    psteps = _like("step_states", step_states, torch.float32, (N, T, ch, shape.state_size), dev)
+    _call(_lib.kda_scan_decode, "kda_scan_decode", dev, stream, *ptrs, pslot, _byref(shape), pout,
+          psteps, pstatus, (capi.KDA_SCAN_SOFTPLUS if softplus else 0)
           | (capi.KDA_LAYER_KEEP_STATE if keep_state else 0))
     return out, step_states
 
@@ -320,47 +318,46 @@ def rms_norm(x, weight=None, *, eps: float = 1e-6, residual=None, gate=None,
     (``group=0``) or per 128 elements (``group=128``): out * scale is the value.
     Returns (out, residual_out, scales); scales [T, (H,) ceil(W / group)].
     """
-    if x.dim() not in (2, 3):
+    full, t, dev = x.shape, x.dtype, _device(x)
+    dims = len(full)
+    if dims not in (2, 3):
         _fail("x: [T, W] or [T, H, W] expected")
-    dev, full = x.device, tuple(x.shape)
-    code = _dtype(x, "x")
-    T, W, H = full[0], full[-1], (full[1] if len(full) == 3 else 1)
-    tail = len(full) - 1
-    _like("weight", weight, torch.float32, (W,), dev)
-    if gate_activation not in _GATES:
+    code, tail = _dtype(x, "x"), dims - 1
+    T, W, H = full[0], full[-1], (full[1] if dims == 3 else 1)
+    pw = _like("weight", weight, torch.float32, (W,), dev)
+    gate_flag = _GATES.get(gate_activation)
+    if gate_flag is None:
         _fail("gate_activation: 'silu' or 'sigmoid'")
-    bits8 = out_dtype == torch.float8_e4m3fn
-    if not bits8 and out_dtype not in (None, x.dtype):
+    bits8 = out_dtype is torch.float8_e4m3fn
+    if not bits8 and out_dtype not in (None, t):
         _fail("out_dtype: x's type or float8_e4m3fn")
     if group not in (0, 128) or (group and not bits8):
         _fail("group: 0, or 128 with an 8-bit output")
     if not bits8 and scales is not None:
         _fail("scales belong to an 8-bit output")
-    otype = torch.float8_e4m3fn if bits8 else x.dtype
+    otype = out_dtype if bits8 else t
     if out is None:
-        out = torch.empty(full, dtype=otype, device=dev)
-    else:
-        _like("out", out, otype, full, dev)
+        out = x.new_empty(full, dtype=otype)
+    pout = _like("out", out, otype, full, dev)
+    xs = _rows("x", x, t, full, dev, tail)
     rs = ros = gs = 0
     if residual is not None:
-        rs = _rows("residual", residual, x.dtype, full, dev, tail)
+        rs = _rows("residual", residual, t, full, dev, tail)
         if residual_out is None:
-            residual_out = torch.empty(full, dtype=x.dtype, device=dev)
-        ros = _rows("residual_out", residual_out, x.dtype, full, dev, tail)
+            residual_out = x.new_empty(full)
+        ros = _rows("residual_out", residual_out, t, full, dev, tail)
     elif residual_out is not None:
         _fail("residual_out needs a residual")
     if gate is not None:
-        gs = _rows("gate", gate, x.dtype, full, dev, tail)
+        gs = _rows("gate", gate, t, full, dev, tail)
+    psc = None
     if bits8:
-        sshape = full[:-1] + (-(-W // 128) if group else 1,)
+        sshape = (*full[:-1], -(-W // 128) if group else 1)
         if scales is None:
-            scales = torch.empty(sshape, dtype=torch.float32, device=dev)
-        else:
-            _like("scales", scales, torch.float32, sshape, dev)
-    shape = capi.kda_norm_shape_t(T, H, W, group, code,
-                                  capi.KDA_DTYPE_E4M3 if bits8 else code,
-                                  _rows("x", x, x.dtype, full, dev, tail), rs, ros, gs, eps, 0)
-    _call(capi.kda_rms_norm, "kda_rms_norm", dev, stream, x.data_ptr(), _ptr(weight),
-          _ptr(residual), _ptr(gate), _byref(shape), out.data_ptr(), _ptr(residual_out),
-          _ptr(scales), _GATES[gate_activation])
+            scales = x.new_empty(sshape, dtype=torch.float32)
+        psc = _like("scales", scales, torch.float32, sshape, dev)
+    shape = capi.kda_norm_shape_t(T, H, W, group, code, capi.KDA_DTYPE_E4M3 if bits8 else code,
+                                  xs, rs, ros, gs, eps, 0)
+    _call(_lib.kda_rms_norm, "kda_rms_norm", dev, stream, x.data_ptr(), pw, _ptr(residual),
+          _ptr(gate), _byref(shape), pout, _ptr(residual_out), psc, gate_flag)
     return out, residual_out, scales
