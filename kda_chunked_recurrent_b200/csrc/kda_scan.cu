@@ -21,6 +21,8 @@
 //
 // Tokens.  Four state elements (16 bytes) per thread, the state read and written once; a
 // CTA takes several sequences so that A stays in registers.
+#include <type_traits>
+
 #include "kda_layer.cuh"
 
 namespace kda {
@@ -30,10 +32,22 @@ namespace scan {
 constexpr int kTB = 32;         // rows per block
 constexpr int kHelpers = 128;   // helper threads
 constexpr int kU = 4;           // rows per step of the scan
-constexpr int kAhead = 6;       // blocks that a row is requested into L2 ahead of its turn
 
-__device__ __forceinline__ void prefetch_l2(const void* p) {
-  asm volatile("prefetch.global.L2 [%0];" ::"l"(p));
+// Asynchronous copy of kBytes (4, 8 or a multiple of 16) from global to shared memory, or of
+// as many zeros.
+template <int kBytes>
+__device__ __forceinline__ void copy_async(uint32_t dst, const void* src, bool zero) {
+  constexpr int kStep = kBytes >= 16 ? 16 : kBytes;
+#pragma unroll
+  for (int o = 0; o < kBytes; o += kStep)
+    asm volatile("cp.async.ca.shared.global [%0], [%1], %2, %3;" ::"r"(dst + o),
+                 "l"(static_cast<const char*>(src) + o), "n"(kStep), "r"(zero ? 0 : kStep)
+                 : "memory");
+}
+__device__ __forceinline__ void copy_commit() { asm volatile("cp.async.commit_group;" ::: "memory"); }
+template <int kPending>
+__device__ __forceinline__ void copy_wait() {
+  asm volatile("cp.async.wait_group %0;" ::"n"(kPending) : "memory");
 }
 
 // log(1 + e^v) = max(v, 0) + log(1 + e), e = e^-|v| in (0, 1], with the logarithm from the
@@ -66,8 +80,9 @@ struct Cfg {
   static constexpr int kCW = 32 / kL;                   // channels side by side in a warp
   static constexpr int kCH = kSW * kCW * kK;            // channels per CTA
   static constexpr int kThreads = 32 * kSW + kHelpers;
-  // a helper thread has two rows of kE channels, and kQ elements of one row of B and of C
-  static constexpr int kE = kCH / 8, kQ = kNP / 4;
+  // a helper thread has two rows of kE channels, kParts threads a row, and kQ elements of one
+  // row of B and of C
+  static constexpr int kE = kCH >= 16 ? kCH / 8 : 2, kParts = kCH / kE, kQ = kNP / 4;
   // row pitch of the sums: a multiple of 4 floats that spreads the four rows which a warp
   // stores together over the banks
   static constexpr int kYP = kCH + (kCH >= 16 ? 8 : 4);
@@ -76,21 +91,30 @@ struct Cfg {
   static constexpr int kLW = kS * 2 * kElem / 4, kRW = kNP * 2 * kElem / 4;
   struct Stage {
     // {d, d} and {d x, d x} of an even row and the next.  Channel part kE + e is at place
-    // 8 e + part, here and in the sums: helper threads write, and scan lanes read, adjacent
-    // places, and a thread's channels stay adjacent in global memory.
+    // kParts e + part, here and in the sums: helper threads write, and scan lanes read,
+    // adjacent places, and a thread's channels stay adjacent in global memory.
     float4 dd[kTB / 2][kCH];
     // B and C in the rows' own type (half the bytes for 16 bits, and it is the reads from
     // shared memory that bound the scan): per lane q its kS elements of B, then of C
     uint32_t bc[kTB][kRW];
   };
   static __device__ __forceinline__ int channel(int place) {
-    return (place % 8) * kE + place / 8;
+    return (place % kParts) * kE + place / kParts;
   }
+  // Rows on their way: what every helper thread copies for itself, kRing blocks deep (as many
+  // as 48 KB hold, at least 4).
+  struct Raws {
+    typename T::Raw x[2][kHelpers][kE], dt[2][kHelpers][kE], z[2][kHelpers][kE];
+    typename T::Raw b[kHelpers][kQ], c[kHelpers][kQ];
+  };
+  static constexpr int kFit = 48 * 1024 / static_cast<int>(sizeof(Raws));
+  static constexpr int kRing = kFit < 4 ? 4 : kFit > 8 ? 8 : kFit;
   struct Smem {
+    Raws raw[kRing];
     Stage st[2];
     float y[2][kTB][kYP];
   };
-  static_assert(kCH % 8 == 0 && kL >= 4, "eight helper parts; the exchange of four rows");
+  static_assert(kCH % 8 == 0 && kL >= 4, "helper parts; the exchange of four rows");
 };
 
 // 2^y on the FMA pipe: y = n + f, |f| <= 1/2, 2^f = 1 + f P(f) with P of degree 4 fitted for
@@ -227,13 +251,6 @@ __device__ __forceinline__ void scan_block(const typename C::Stage& st, float (&
   }
 }
 
-// What a helper thread holds of a block: two rows of its channels, part of a row of B and C.
-template <typename T, typename C>
-struct Block {
-  Vec<T, C::kE> x[2], dt[2];
-  Vec<T, C::kQ> b, c;
-};
-
 // kVec: the rows' vectors may be moved whole (then a part is inside the tile or outside).
 template <typename T, typename C, bool kVec>
 __global__ void __launch_bounds__(C::kThreads) kda_scan_prefill_kernel(const ScanParams p) {
@@ -300,22 +317,22 @@ __global__ void __launch_bounds__(C::kThreads) kda_scan_prefill_kernel(const Sca
   // ---- helper warps: rows 2 rp and 2 rp + 1 of a block, channels part kE .. + kE - 1; row br
   // of B and C, elements quarter kQ .. + kQ - 1
   const int ht = tid - 32 * C::kSW;
-  const int rp = ht >> 3, part = ht & 7, br = ht >> 2, quarter = ht & 3;
-  const int cl = part * kE, left = nch - cl;      // channels of this thread in the tile
+  const int rp = ht / C::kParts, part = ht % C::kParts, br = ht >> 2, quarter = ht & 3;
+  const int cl = part * kE;
+  const int left = rp < kTB / 2 ? nch - cl : 0;      // channels of this thread in the tile
   const int left_bc = p.size - quarter * kQ;
   const bool gated = p.z != nullptr;
   const auto rows_at = [&](const void* base, int64_t stride, int64_t row, int64_t off) {
     return static_cast<const Raw*>(base) + row * stride + off;
   };
-  // rows of the block that is loaded next
+  // rows of the block that is copied next
   const int64_t lrow = static_cast<int64_t>(row0) + 2 * rp, brow = static_cast<int64_t>(row0) + br;
   const Raw* X = rows_at(p.x, p.xs, lrow, cbase + cl);
   const Raw* DT = rows_at(p.dt, p.ds, lrow, cbase + cl);
+  const Raw* Z = rows_at(p.z, p.zs, lrow, cbase + cl);
   const Raw* Bp = rows_at(p.B, p.bs, brow, static_cast<int64_t>(grp) * p.size + quarter * kQ);
   const Raw* Cp = rows_at(p.Cm, p.cs, brow, static_cast<int64_t>(grp) * p.size + quarter * kQ);
-  // rows of the block that is written next
-  const Raw* FX = X;
-  const Raw* Z = gated ? rows_at(p.z, p.zs, lrow, cbase + cl) : nullptr;
+  // row of the block that is written next
   Raw* O = static_cast<Raw*>(p.out) + lrow * p.channels + cbase + cl;
   float2 bias[kE];
 #pragma unroll
@@ -326,59 +343,82 @@ __global__ void __launch_bounds__(C::kThreads) kda_scan_prefill_kernel(const Sca
   for (int e = 0; e < kE; ++e)
     skip[e] = (p.D != nullptr && e < left) ? p.D[cbase + cl + e] : 0.f;
 
-  const auto load = [&](int b, Block<T, C>& k) {
-    const int rest = len - b * kTB;      // rows from the block's first on
-#pragma unroll
-    for (int o = 0; o < 2; ++o) {
-      if (left > 0 && 2 * rp + o < rest) {
-        k.x[o].template load<kVec>(X + o * p.xs, left);
-        k.dt[o].template load<kVec>(DT + o * p.ds, left);
-      } else {
-        k.x[o].clear();
-        k.dt[o].clear();
-      }
-    }
-    if (left_bc > 0 && br < rest) {
-      k.b.template load<kVec>(Bp, left_bc);
-      k.c.template load<kVec>(Cp, left_bc);
+  // Ask for a thread's rows of block b (zeros where there are none).  Without the vectors'
+  // alignment the elements go through registers.
+  const auto bring = [&](auto n_c, Raw* dst, const Raw* src, const void* base, int count) {
+    constexpr int kN = decltype(n_c)::value;
+    if constexpr (kVec) {
+      copy_async<kN * static_cast<int>(sizeof(Raw))>(smem_u32(dst), count > 0 ? src : base,
+                                                     count <= 0);
     } else {
-      k.b.clear();
-      k.c.clear();
+      Vec<T, kN> v;
+      v.template load<false>(src, count);
+      v.template store<true>(dst);
     }
-    X += kTB * p.xs;
-    DT += kTB * p.ds;
-    Bp += kTB * p.bs;
-    Cp += kTB * p.cs;
+  };
+  using NE = std::integral_constant<int, kE>;
+  using NQ = std::integral_constant<int, kQ>;
+  const auto request = [&](int b) {
+    if (b < nblk) {
+      typename C::Raws& r = sm.raw[b % C::kRing];
+      const int rest = len - b * kTB;      // rows from the block's first on
+#pragma unroll
+      for (int o = 0; o < 2; ++o) {
+        const int count = 2 * rp + o < rest ? left : 0;
+        bring(NE(), r.x[o][ht], X + o * p.xs, p.x, count);
+        bring(NE(), r.dt[o][ht], DT + o * p.ds, p.dt, count);
+        if (gated) bring(NE(), r.z[o][ht], Z + o * p.zs, p.z, count);
+      }
+      const int count = br < rest ? left_bc : 0;
+      bring(NQ(), r.b[ht], Bp, p.B, count);
+      bring(NQ(), r.c[ht], Cp, p.Cm, count);
+      X += kTB * p.xs;
+      DT += kTB * p.ds;
+      Z += kTB * p.zs;
+      Bp += kTB * p.bs;
+      Cp += kTB * p.cs;
+    }
+    copy_commit();
   };
   // rows past the sequence get d = 0: the state stays, their sums are not used
-  const auto stage = [&](int b, const Block<T, C>& k) {
+  const auto stage = [&](int b) {
     typename C::Stage& st = sm.st[b & 1];
+    const typename C::Raws& raw = sm.raw[b % C::kRing];
     const int rest = len - b * kTB - 2 * rp;
-    float x0[kE], x1[kE], d0[kE], d1[kE];
-    k.x[0].unpack(x0);
-    k.x[1].unpack(x1);
-    k.dt[0].unpack(d0);
-    k.dt[1].unpack(d1);
+    if (rp < kTB / 2) {
+      float x[2][kE], dt[2][kE];
 #pragma unroll
-    for (int e = 0; e < kE; ++e) {
-      float2 d = add2<true>(make_float2(d0[e], d1[e]), bias[e]);
-      if (p.softplus) d = softplus2(d);
-      if (rest < 2) d = make_float2(rest > 0 ? d.x : 0.f, 0.f);
-      const float2 dx = mul2<true>(d, make_float2(x0[e], x1[e]));
-      st.dd[rp][8 * e + part] = make_float4(d.x, d.y, dx.x, dx.y);
+      for (int o = 0; o < 2; ++o) {
+        Vec<T, kE> v;
+        v.template load<true>(raw.x[o][ht]);
+        v.unpack(x[o]);
+        v.template load<true>(raw.dt[o][ht]);
+        v.unpack(dt[o]);
+      }
+#pragma unroll
+      for (int e = 0; e < kE; ++e) {
+        float2 d = add2<true>(make_float2(dt[0][e], dt[1][e]), bias[e]);
+        if (p.softplus) d = softplus2(d);
+        if (rest < 2) d = make_float2(rest > 0 ? d.x : 0.f, 0.f);
+        const float2 dx = mul2<true>(d, make_float2(x[0][e], x[1][e]));
+        st.dd[rp][C::kParts * e + part] = make_float4(d.x, d.y, dx.x, dx.y);
+      }
     }
     // the words of kQ elements: kS of B, kS of C, lane by lane
     constexpr int kWords = kQ * 2 * C::kElem / 4, kHalf = C::kLW / 2;
+    Vec<T, kQ> vb, vc;
+    vb.template load<true>(raw.b[ht]);
+    vc.template load<true>(raw.c[ht]);
     uint32_t w[kWords];
     if constexpr (kHalf == 0) {     // one element of 16 bits each: B low, C high
 #pragma unroll
       for (int i = 0; i < kWords; ++i)
-        w[i] = __byte_perm(k.b.w[i / 2], k.c.w[i / 2], i % 2 ? 0x7632 : 0x5410);
+        w[i] = __byte_perm(vb.w[i / 2], vc.w[i / 2], i % 2 ? 0x7632 : 0x5410);
     } else {
 #pragma unroll
       for (int i = 0; i < kWords / 2; ++i) {
-        w[i / kHalf * C::kLW + i % kHalf] = k.b.w[i];
-        w[i / kHalf * C::kLW + kHalf + i % kHalf] = k.c.w[i];
+        w[i / kHalf * C::kLW + i % kHalf] = vb.w[i];
+        w[i / kHalf * C::kLW + kHalf + i % kHalf] = vc.w[i];
       }
     }
     uint4* to = reinterpret_cast<uint4*>(&st.bc[br][quarter * kWords]);
@@ -386,43 +426,30 @@ __global__ void __launch_bounds__(C::kThreads) kda_scan_prefill_kernel(const Sca
     for (int i = 0; i < kWords / 4; ++i)
       to[i] = make_uint4(w[4 * i], w[4 * i + 1], w[4 * i + 2], w[4 * i + 3]);
   };
-  // x and z of the block to be written, loaded a while before
-  Vec<T, kE> fx[2], fz[2];
-  const auto finish_load = [&](int b) {
-    const int rest = len - b * kTB - 2 * rp;
-#pragma unroll
-    for (int o = 0; o < 2; ++o)
-      if (left > 0 && o < rest) {
-        fx[o].template load<kVec>(FX + o * p.xs, left);
-        if (gated) fz[o].template load<kVec>(Z + o * p.zs, left);
-      }
-    FX += kTB * p.xs;
-    if (gated) Z += kTB * p.zs;
-  };
   const auto finish = [&](int b) {
+    const typename C::Raws& raw = sm.raw[b % C::kRing];
     const int rest = len - b * kTB - 2 * rp;
     if (left > 0) {
 #pragma unroll
       for (int o = 0; o < 2; ++o) {
         if (o >= rest) break;
         float xf[kE], zf[kE], y[kE];
-        fx[o].unpack(xf);
+        Vec<T, kE> v;
+        v.template load<true>(raw.x[o][ht]);
+        v.unpack(xf);
 #pragma unroll
-        for (int e = 0; e < kE; ++e) y[e] = fmaf(skip[e], xf[e], sm.y[b & 1][2 * rp + o][8 * e + part]);
+        for (int e = 0; e < kE; ++e)
+          y[e] = fmaf(skip[e], xf[e], sm.y[b & 1][2 * rp + o][C::kParts * e + part]);
         if (gated) {
-          fz[o].unpack(zf);
-          if constexpr (kE == 1) {
-            y[0] *= zf[0] * sigmoid(zf[0]);
-          } else {
+          v.template load<true>(raw.z[o][ht]);
+          v.unpack(zf);
 #pragma unroll
-            for (int e = 0; e < kE; e += 2) {
-              const float2 g = silu2(make_float2(zf[e], zf[e + 1]));
-              y[e] *= g.x;
-              y[e + 1] *= g.y;
-            }
+          for (int e = 0; e < kE; e += 2) {
+            const float2 g = silu2(make_float2(zf[e], zf[e + 1]));
+            y[e] *= g.x;
+            y[e + 1] *= g.y;
           }
         }
-        Vec<T, kE> v;
         v.pack(y);
         v.template store<kVec>(O + static_cast<int64_t>(o) * p.channels, left);
       }
@@ -430,58 +457,25 @@ __global__ void __launch_bounds__(C::kThreads) kda_scan_prefill_kernel(const Sca
     O += static_cast<int64_t>(kTB) * p.channels;
   };
 
-  // Rows come from HBM long before their turn: a thread asks for row br of x, dt, z, or of B
-  // and C, kAhead blocks ahead of the loads, which then find them in L2.
-  const Raw* ahead[2] = {nullptr, nullptr};
-  {
-    const int64_t row = brow + kAhead * kTB;
-    if (quarter == 0) ahead[0] = rows_at(p.x, p.xs, row, cbase);
-    if (quarter == 1) ahead[0] = rows_at(p.dt, p.ds, row, cbase);
-    if (quarter == 2 && gated) ahead[0] = rows_at(p.z, p.zs, row, cbase);
-    if (quarter == 3) {
-      ahead[0] = rows_at(p.B, p.bs, row, static_cast<int64_t>(grp) * p.size);
-      ahead[1] = rows_at(p.Cm, p.cs, row, static_cast<int64_t>(grp) * p.size);
-    }
-  }
-  const int64_t ahead_step =
-      kTB * (quarter == 0 ? p.xs : quarter == 1 ? p.ds : quarter == 2 ? p.zs : p.bs);
-  const int ahead_bytes = (quarter < 3 ? nch : p.size) * C::kElem;
-  const auto request = [&](int b) {      // the rows of block b + kAhead
-    if (ahead[0] != nullptr && (b + kAhead) * kTB + br < len) {
-      for (int o = 0; o < ahead_bytes; o += 128) {
-        prefetch_l2(reinterpret_cast<const char*>(ahead[0]) + o);
-        if (quarter == 3) prefetch_l2(reinterpret_cast<const char*>(ahead[1]) + o);
-      }
-    }
-    if (ahead[0] != nullptr) ahead[0] += ahead_step;
-    if (quarter == 3) ahead[1] += kTB * p.cs;
-  };
-
-  Block<T, C> k0, k1;
-  if (nblk > 0) {
-    load(0, k0);
-    if (nblk > 1) load(1, k1);
-    stage(0, k0);
-  }
+  // Slot b % kRing holds block b from its request to its output, so blocks b - 1 to
+  // b + kRing - 2 are there in turn b.  A thread reads back only what it copied itself: its
+  // own wait is all the ordering that needs.
+  constexpr int kPending = C::kRing - 3;
+  for (int b = 0; b < C::kRing - 2; ++b) request(b);
+  copy_wait<kPending>();
+  if (nblk > 0) stage(0);
   __syncthreads();
-  // Turn b, beside the scan of block b: block b + 2 is requested, block b + 1 (requested a
-  // turn ago) staged, block b - 1 written.
-  const auto turn = [&](int b, Block<T, C>& next, Block<T, C>& after) {
-    request(b);
-    if (b > 0) finish_load(b - 1);
-    if (b + 2 < nblk) load(b + 2, after);
-    if (b + 1 < nblk) stage(b + 1, next);
+  // Turn b, beside the scan of block b: block b + kRing - 2 is asked for, block b + 1 staged,
+  // block b - 1 written.
+  for (int b = 0; b < nblk; ++b) {
+    request(b + C::kRing - 2);
+    copy_wait<kPending>();
+    if (b + 1 < nblk) stage(b + 1);
     if (b > 0) finish(b - 1);
     __syncthreads();
-  };
-  for (int b = 0; b < nblk; b += 2) {
-    turn(b, k1, k0);
-    if (b + 1 < nblk) turn(b + 1, k0, k1);
   }
-  if (nblk > 0) {
-    finish_load(nblk - 1);
-    finish(nblk - 1);
-  }
+  copy_wait<0>();
+  if (nblk > 0) finish(nblk - 1);
 }
 
 // ---- tokens: four elements per lane, kL lanes per channel, four sequences at a time.
