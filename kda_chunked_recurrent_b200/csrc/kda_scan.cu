@@ -13,14 +13,19 @@
 // Prompts.  A CTA takes one sequence and a tile of channels through all its rows, the state
 // in registers.  A channel's elements lie on kL lanes, kS a lane, so that one sequence of a
 // few thousand channels already fills the SMs.  Four scan warps do nothing but the
-// recurrence; four helper warps, one block of kTB rows ahead, load the next rows, form d and
-// d x once per (row, channel) and the FP32 rows of B and C in shared memory, and, one block
-// behind, turn the sums into output rows (skip, gate, rounding).  One barrier a block.
-// The sum over a channel's lanes is done for four rows at a time: two exchange steps leave
-// each lane with one row's sum (three shuffles for four rows).
+// recurrence.  Four helper warps copy rows into a ring of raw blocks of kTB rows several
+// blocks ahead (a row of HBM is about a microsecond away, as long as two blocks take), form d
+// and d x once per (row, channel) one block ahead, and, one block behind, add the lanes' parts
+// of the sums and write the output rows (skip, gate, rounding).  One barrier a block.
+// Special functions and shared-memory reads go through one queue and their times add up:
+// 4096 channels, per row and scan warp, about 33 clocks for 4 exponentials a lane and 22 for
+// the reads of B, C, d and d x.  So B and C stay in the rows' own type, and the sums are not
+// exchanged between the lanes.  An exponential in eight on the FMA pipe cost more issue slots
+// than it saved (312 -> 337 us), two channels per lane sharing their B and C too many
+// registers and too much shared memory for a second CTA on the SM (401 -> 419 us).
 //
 // Tokens.  Four state elements (16 bytes) per thread, the state read and written once; a
-// CTA takes several sequences so that A stays in registers.
+// CTA takes four sequences so that A is read once for them.
 #include <type_traits>
 
 #include "kda_layer.cuh"
@@ -30,8 +35,10 @@ namespace layer {
 namespace scan {
 
 constexpr int kTB = 32;         // rows per block
+constexpr int kSW = 4;          // scan warps
 constexpr int kHelpers = 128;   // helper threads
-constexpr int kU = 4;           // rows per step of the scan
+constexpr int kThreads = 32 * kSW + kHelpers;
+constexpr int kU = 2;           // rows per step of the scan
 
 // Asynchronous copy of kBytes (4, 8 or a multiple of 16) from global to shared memory, or of
 // as many zeros.
@@ -53,12 +60,13 @@ __device__ __forceinline__ void copy_wait() {
 // log(1 + e^v) = max(v, 0) + log(1 + e), e = e^-|v| in (0, 1], with the logarithm from the
 // series of the inverse hyperbolic tangent, log(1 + e) = 2 atanh(s), s = e / (2 + e) <= 1/3,
 // which is relatively exact for a small e too (a step of 1e-3 is the usual case, and its
-// relative error is the state's): the first term left out is s^15 / 15, below 2^-27 of s.
+// relative error is the state's): the first term left out is s^15 / 15, below 2^-26 of s.
 __device__ __forceinline__ float2 splat(float v) { return make_float2(v, v); }
 __device__ __forceinline__ float2 softplus2(float2 v) {
   const float2 e = make_float2(ex2(-fabsf(v.x) * kLog2e), ex2(-fabsf(v.y) * kLog2e));
   const float2 t = add2<true>(e, splat(2.f));
-  const float2 s = mul2<true>(e, make_float2(rcp_approx(t.x), rcp_approx(t.y)));
+  const float r2 = rcp_approx(t.x * t.y);      // both reciprocals from one (2 <= t <= 3)
+  const float2 s = mul2<true>(e, make_float2(r2 * t.y, r2 * t.x));
   const float2 q = mul2<true>(s, s);
   float2 r = fma2<true>(q, splat(1.f / 13.f), splat(1.f / 11.f));
   r = fma2<true>(q, r, splat(1.f / 9.f));
@@ -70,22 +78,20 @@ __device__ __forceinline__ float2 softplus2(float2 v) {
 }
 __device__ __forceinline__ float softplus(float v) { return softplus2(make_float2(v, 0.f)).x; }
 
-// kNP state elements per channel (padded), kS of them per lane, kK channels per lane, kSW scan
-// warps; kPoly of the kU kS / 2 pairs of exponentials of a step and channel have one on the
-// FMA pipe.
-template <typename T, int kNP_, int kS_, int kK_, int kSW_, int kPoly_ = 0>
+// kNP state elements per channel (padded), kS of them per lane.
+template <typename T, int kNP_, int kS_>
 struct Cfg {
-  static constexpr int kNP = kNP_, kS = kS_, kK = kK_, kSW = kSW_, kPoly = kPoly_;
+  static constexpr int kNP = kNP_, kS = kS_;
   static constexpr int kL = kNP / kS;                   // lanes per channel
   static constexpr int kCW = 32 / kL;                   // channels side by side in a warp
-  static constexpr int kCH = kSW * kCW * kK;            // channels per CTA
-  static constexpr int kThreads = 32 * kSW + kHelpers;
+  static constexpr int kCH = kSW * kCW;                 // channels per CTA
   // a helper thread has two rows of kE channels, kParts threads a row, and kQ elements of one
   // row of B and of C
   static constexpr int kE = kCH >= 16 ? kCH / 8 : 2, kParts = kCH / kE, kQ = kNP / 4;
-  // row pitch of the sums: a multiple of 4 floats that spreads the four rows which a warp
-  // stores together over the banks
-  static constexpr int kYP = kCH + (kCH >= 16 ? 8 : 4);
+  // the lanes' parts of the sums of a pair of rows, two lanes side by side
+  struct Sums {
+    float2 part[kTB / 2][kL / 2][kCH][2];
+  };
   // 32-bit words of B (as many of C) that a lane reads per row, and of a row of both
   static constexpr int kElem = sizeof(typename T::Raw);
   static constexpr int kLW = kS * 2 * kElem / 4, kRW = kNP * 2 * kElem / 4;
@@ -102,42 +108,28 @@ struct Cfg {
     return (place % kParts) * kE + place / kParts;
   }
   // Rows on their way: what every helper thread copies for itself, kRing blocks deep (as many
-  // as 48 KB hold, at least 4).
+  // as 32 KB hold; at least 4, or 3 of the largest, whose copies then overlap one block only).
   struct Raws {
     typename T::Raw x[2][kHelpers][kE], dt[2][kHelpers][kE], z[2][kHelpers][kE];
     typename T::Raw b[kHelpers][kQ], c[kHelpers][kQ];
   };
-  static constexpr int kFit = 48 * 1024 / static_cast<int>(sizeof(Raws));
-  static constexpr int kRing = kFit < 4 ? 4 : kFit > 8 ? 8 : kFit;
+  static constexpr int kFit = 32 * 1024 / static_cast<int>(sizeof(Raws));
+  static constexpr int kLeast = sizeof(Raws) > 32 * 1024 ? 3 : 4;
+  static constexpr int kRing = kFit < kLeast ? kLeast : kFit > 8 ? 8 : kFit;
   struct Smem {
     Raws raw[kRing];
     Stage st[2];
-    float y[2][kTB][kYP];
+    Sums y[2];     // (16-byte aligned: what precedes is whole vectors)
   };
-  static_assert(kCH % 8 == 0 && kL >= 4, "helper parts; the exchange of four rows");
+  static_assert(sizeof(Smem) <= 227 * 1024, "shared memory of a CTA");
+  static_assert(kCH % 8 == 0 && kL >= 4, "helper parts; pairs of lanes");
 };
-
-// 2^y on the FMA pipe: y = n + f, |f| <= 1/2, 2^f = 1 + f P(f) with P of degree 4 fitted for
-// the least relative error of 2^f (9e-8 before rounding); n goes into the exponent.  y is
-// taken to [-126, 128]: below, the decay is 2^-126; at 128 the result is infinite.
-__device__ __forceinline__ float ex2_fma(float y) {
-  y = fminf(fmaxf(y, -126.f), 128.f);
-  const float big = 12582912.f;   // 1.5 * 2^23: adding it rounds to an integer
-  const float t = y + big, f = y - (t - big);
-  float r = fmaf(f, 0.001326472731307149f, 0.009671512991189957f);
-  r = fmaf(f, r, 0.05550733581185341f);
-  r = fmaf(f, r, 0.24022242426872253f);
-  r = fmaf(f, r, 0.6931470036506653f);
-  r = fmaf(f, r, 1.f);
-  return __uint_as_float(__float_as_uint(r) + (__float_as_uint(t) << 23));
-}
 
 // The operands of kU rows for one lane, read from a stage.
 template <typename T, typename C>
 struct Rows {
-  static constexpr int kP = C::kS / 2 + (C::kS == 1);    // pairs of elements
   uint32_t bc[kU][C::kLW];
-  float4 dd[C::kK][kU / 2];
+  float4 dd[kU / 2];
   __device__ __forceinline__ void load(const typename C::Stage& st, int t, int ch0, int q) {
 #pragma unroll
     for (int u = 0; u < kU; ++u) {
@@ -151,117 +143,127 @@ struct Rows {
           bc[u][4 * i + 2] = v.z;
           bc[u][4 * i + 3] = v.w;
         }
-      } else if constexpr (C::kLW == 2) {
+      } else {
         const uint2 v = *reinterpret_cast<const uint2*>(w);
         bc[u][0] = v.x;
         bc[u][1] = v.y;
-      } else {
-        bc[u][0] = *w;
       }
     }
 #pragma unroll
-    for (int k = 0; k < C::kK; ++k)
-#pragma unroll
-      for (int u = 0; u < kU; u += 2) dd[k][u / 2] = st.dd[(t + u) / 2][ch0 + k * C::kCW];
+    for (int u = 0; u < kU; u += 2) dd[u / 2] = st.dd[(t + u) / 2][ch0];
   }
-  // elements 2 i and 2 i + 1 of B (of C), element 0 for kS == 1
+  // elements 2 i and 2 i + 1 of B (of C)
   __device__ __forceinline__ float2 pair(int u, int i, bool c) const {
     if constexpr (C::kElem == 4) {
-      const uint32_t* w = &bc[u][c ? C::kS : 0];
-      return make_float2(__uint_as_float(w[2 * i]), C::kS == 1 ? 0.f : __uint_as_float(w[2 * i + 1]));
-    } else if constexpr (C::kS == 1) {
-      const float2 v = T::unpack2(bc[u][0]);
-      return make_float2(c ? v.y : v.x, 0.f);
+      const uint32_t* w = &bc[u][(c ? C::kS : 0) + 2 * i];
+      return make_float2(__uint_as_float(w[0]), __uint_as_float(w[1]));
     } else {
       return T::unpack2(bc[u][(c ? C::kLW / 2 : 0) + i]);
     }
   }
 };
 
-// kU rows of the recurrence: h moves on, sum[k][u] is the lane's part of the read-out.
-template <typename T, typename C>
-__device__ __forceinline__ void step_rows(const Rows<T, C>& r, float (&h)[C::kK][C::kS],
-                                          const float (&A)[C::kK][C::kS], float (&sum)[C::kK][kU]) {
-#pragma unroll
-  for (int k = 0; k < C::kK; ++k) {
-#pragma unroll
-    for (int u = 0; u < kU; ++u) {
-      const float4 dd = r.dd[k][u / 2];
-      const float d = u % 2 ? dd.y : dd.x, dx = u % 2 ? dd.w : dd.z;
-      if constexpr (C::kS == 1) {
-        h[k][0] = fmaf(ex2(d * A[k][0]), h[k][0], dx * r.pair(u, 0, false).x);
-        sum[k][u] = r.pair(u, 0, true).x * h[k][0];
-      } else {
-        float2 acc;
-#pragma unroll
-        for (int i = 0; i < C::kS; i += 2) {
-          const float2 y = mul2<true>(make_float2(d, d), make_float2(A[k][i], A[k][i + 1]));
-          const bool fma_pipe = ((u * (C::kS / 2) + i / 2) * C::kPoly) % (kU * C::kS / 2) <
-                                                    C::kPoly;
-          const float2 a = make_float2(ex2(y.x), fma_pipe ? ex2_fma(y.y) : ex2(y.y));
-          const float2 b = mul2<true>(make_float2(dx, dx), r.pair(u, i / 2, false));
-          const float2 n = fma2<true>(a, make_float2(h[k][i], h[k][i + 1]), b);
-          h[k][i] = n.x;
-          h[k][i + 1] = n.y;
-          const float2 c = r.pair(u, i / 2, true);
-          acc = i == 0 ? mul2<true>(c, n) : fma2<true>(c, n, acc);
-        }
-        sum[k][u] = acc.x + acc.y;
-      }
-    }
-  }
-}
-
-// Sums of kU rows over the kL lanes of a channel: in two exchanges the lanes q, q^1, q^2, q^3
-// are left with row q & 3 each, then the other lanes are added.
+// What a step needs of its rows besides the state: decays, inputs, and C.
 template <typename C>
-__device__ __forceinline__ void reduce_rows(const float (&sum)[C::kK][kU],
-                                            float (&yb)[kTB][C::kYP], int t, int ch0, int q) {
-  const bool b0 = q & 1, b1 = q & 2;
+struct Ops {
+  static constexpr int kP = C::kS / 2;      // pairs of elements
+  float2 a[kU][kP], b[kU][kP], c[kU][kP];
+};
+
+// Row u's decays, inputs and C.
+template <typename T, typename C>
+__device__ __forceinline__ void prepare_row(const Rows<T, C>& r, const float (&A)[C::kS],
+                                            Ops<C>& o, int u) {
+  const float4 dd = r.dd[u / 2];
+  const float d = u % 2 ? dd.y : dd.x, dx = u % 2 ? dd.w : dd.z;
 #pragma unroll
-  for (int k = 0; k < C::kK; ++k) {
-    const float p0 = (b0 ? sum[k][1] : sum[k][0]) +
-                     __shfl_xor_sync(0xffffffffu, b0 ? sum[k][0] : sum[k][1], 1);
-    const float p1 = (b0 ? sum[k][3] : sum[k][2]) +
-                     __shfl_xor_sync(0xffffffffu, b0 ? sum[k][2] : sum[k][3], 1);
-    float v = (b1 ? p1 : p0) + __shfl_xor_sync(0xffffffffu, b1 ? p0 : p1, 2);
-#pragma unroll
-    for (int o = 4; o < C::kL; o <<= 1) v += __shfl_xor_sync(0xffffffffu, v, o);
-    if (q < 4) yb[t + q][ch0 + k * C::kCW] = v;
+  for (int i = 0; i < Ops<C>::kP; ++i) {
+    const float2 y = mul2<true>(splat(d), make_float2(A[2 * i], A[2 * i + 1]));
+    o.a[u][i] = make_float2(ex2(y.x), ex2(y.y));
+    o.b[u][i] = mul2<true>(splat(dx), r.pair(u, i, false));
+    o.c[u][i] = r.pair(u, i, true);
   }
 }
 
-// One block's scan by one warp, two groups of kU rows a turn: the next group's operands are
-// read while one is worked on, so that a scheduler with a single scan warp is kept busy.
-// Rows from nt on have d = 0 and B = C = 0 and change nothing.
+// Row u of the recurrence: h moves on; the lane's part of the read-out is returned.
+template <typename C>
+__device__ __forceinline__ float run_row(const Ops<C>& o, float2 (&h)[Ops<C>::kP], int u) {
+  float2 acc;
+#pragma unroll
+  for (int i = 0; i < Ops<C>::kP; ++i) {
+    h[i] = fma2<true>(o.a[u][i], h[i], o.b[u][i]);
+    acc = i == 0 ? mul2<true>(o.c[u][0], h[0]) : fma2<true>(o.c[u][i], h[i], acc);
+  }
+  return acc.x + acc.y;
+}
+
+// One block's scan by one warp.  A scheduler may have a single scan warp, so its instructions
+// are interleaved here: beside the recurrence of one step stand the exponentials of the next
+// and the shared-memory reads of the one after.  Rows from nt on have d = 0 and B = C = 0 and
+// change nothing.
 template <typename T, typename C>
-__device__ __forceinline__ void scan_block(const typename C::Stage& st, float (&yb)[kTB][C::kYP],
-                                           float (&h)[C::kK][C::kS], const float (&A)[C::kK][C::kS],
+__device__ __forceinline__ void scan_block(const typename C::Stage& st, typename C::Sums& y,
+                                           float2 (&h)[Ops<C>::kP], const float (&A)[C::kS],
                                            int ch0, int q, int nt) {
   Rows<T, C> r0, r1;
-  float s0[C::kK][kU], s1[C::kK][kU];
+  Ops<C> o0, o1;
   r0.load(st, 0, ch0, q);
+  r1.load(st, kU, ch0, q);
+#pragma unroll
+  for (int u = 0; u < kU; ++u) prepare_row<T, C>(r0, A, o0, u);
+  const auto step = [&](int t, Rows<T, C>& far, const Rows<T, C>& near, Ops<C>& next,
+                        const Ops<C>& now) {
+    float sum[kU];
+    far.load(st, (t + 2 * kU) % kTB, ch0, q);
+#pragma unroll
+    for (int u = 0; u < kU; ++u) {
+      prepare_row<T, C>(near, A, next, u);
+      sum[u] = run_row<C>(now, h, u);
+    }
+    // The lane's parts of the sums as they are: the helper that writes the rows adds the kL
+    // parts (cheaper than exchanging them between the scan's lanes).
+#pragma unroll
+    for (int u = 0; u < kU; u += 2)
+      y.part[(t + u) / 2][q / 2][ch0][q % 2] = make_float2(sum[u], sum[u + 1]);
+  };
   for (int t = 0; t < nt; t += 2 * kU) {
-    r1.load(st, t + kU, ch0, q);
-    step_rows<T, C>(r0, h, A, s0);
-    r0.load(st, (t + 2 * kU) % kTB, ch0, q);
-    reduce_rows<C>(s0, yb, t, ch0, q);
-    step_rows<T, C>(r1, h, A, s1);
-    reduce_rows<C>(s1, yb, t + kU, ch0, q);
+    step(t, r0, r1, o1, o0);
+    step(t + kU, r1, r0, o0, o1);
   }
 }
 
 // kVec: the rows' vectors may be moved whole (then a part is inside the tile or outside).
 template <typename T, typename C, bool kVec>
-__global__ void __launch_bounds__(C::kThreads) kda_scan_prefill_kernel(const ScanParams p) {
+__global__ void __launch_bounds__(kThreads, 2) kda_scan_prefill_kernel(const ScanParams p) {
   using Raw = typename T::Raw;
   constexpr int kE = C::kE, kQ = C::kQ;
   extern __shared__ __align__(16) uint8_t smem_raw[];
   typename C::Smem& sm = *reinterpret_cast<typename C::Smem*>(smem_raw);
   const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
   const int tiles = p.groups * p.tiles_per_group;
-  const int32_t n = blockIdx.x / tiles;
+  int32_t n = blockIdx.x / tiles;
   const int tile = blockIdx.x - n * tiles;
+  // Ragged batches: the longest sequences first, so that the last CTAs to start are short.
+  if (p.seq.cu != nullptr && p.seq.num > 1 && p.seq.num <= kThreads) {
+    int32_t* lens = reinterpret_cast<int32_t*>(smem_raw);
+    int32_t* found = lens + kThreads;
+    int32_t mine = 0;
+    if (tid < p.seq.num) {
+      int32_t a, b;
+      p.seq.range(tid, a, b);
+      mine = b - a;
+      lens[tid] = mine;
+    }
+    __syncthreads();
+    if (tid < p.seq.num) {
+      int32_t rank = 0;
+      for (int i = 0; i < p.seq.num; ++i) rank += lens[i] > mine || (lens[i] == mine && i < tid);
+      if (rank == n) *found = tid;
+    }
+    __syncthreads();
+    n = *found;
+    __syncthreads();
+  }
   const int grp = tile / p.tiles_per_group;
   const int in_grp = (tile - grp * p.tiles_per_group) * C::kCH;
   const int cbase = grp * p.per_group + in_grp;              // first channel of the tile
@@ -273,25 +275,23 @@ __global__ void __launch_bounds__(C::kThreads) kda_scan_prefill_kernel(const Sca
       p.state == nullptr ? -1 : state_slot(p.slot, n, p.pool, p.status, tile == 0 && tid == 0);
   if (len == 0 && slot < 0) return;
 
-  if (warp < C::kSW) {
+  if (warp < kSW) {
     // ---- scan warps
-    const int q = lane % C::kL, ch0 = warp * (C::kCW * C::kK) + lane / C::kL;   // place
-    float h[C::kK][C::kS], A[C::kK][C::kS];
+    const int q = lane % C::kL, ch0 = warp * C::kCW + lane / C::kL;   // place
+    const int ch = C::channel(ch0);
+    float2 h[Ops<C>::kP];
+    float A[C::kS];
     const bool old = slot >= 0 && (p.has == nullptr || p.has[n] != 0);
+    const int64_t at = static_cast<int64_t>(cbase + ch) * p.size + q * C::kS;
+    float* state = p.state + static_cast<int64_t>(slot) * p.channels * p.size + at;
 #pragma unroll
-    for (int k = 0; k < C::kK; ++k) {
-      const int ch = C::channel(ch0 + k * C::kCW);
-#pragma unroll
-      for (int i = 0; i < C::kS; ++i) {
-        const int e = q * C::kS + i;
-        const bool in = ch < nch && e < p.size;
-        const int64_t at = static_cast<int64_t>(cbase + ch) * p.size + e;
-        // elements past the state's size decay at rate 0 and take nothing: B and C are 0 there
-        A[k][i] = in ? -expf(p.A_log[at]) * kLog2e : 0.f;
-        h[k][i] = (in && old)
-                      ? p.state[static_cast<int64_t>(slot) * p.channels * p.size + at]
-                      : 0.f;
-      }
+    for (int i = 0; i < C::kS; ++i) {
+      const bool in = ch < nch && q * C::kS + i < p.size;
+      // elements past the state's size decay at rate 0 and take nothing: B and C are 0 there
+      A[i] = in ? -expf(p.A_log[at + i]) * kLog2e : 0.f;
+      const float v = (in && old) ? state[i] : 0.f;
+      if (i % 2 == 0) h[i / 2].x = v;
+      else h[i / 2].y = v;
     }
     __syncthreads();
     for (int b = 0; b < nblk; ++b) {
@@ -300,23 +300,15 @@ __global__ void __launch_bounds__(C::kThreads) kda_scan_prefill_kernel(const Sca
     }
     if (slot >= 0) {
 #pragma unroll
-      for (int k = 0; k < C::kK; ++k) {
-        const int ch = C::channel(ch0 + k * C::kCW);
-#pragma unroll
-        for (int i = 0; i < C::kS; ++i) {
-          const int e = q * C::kS + i;
-          if (ch < nch && e < p.size)
-            p.state[(static_cast<int64_t>(slot) * p.channels + cbase + ch) * p.size + e] =
-                h[k][i];
-        }
-      }
+      for (int i = 0; i < C::kS; ++i)
+        if (ch < nch && q * C::kS + i < p.size) state[i] = i % 2 == 0 ? h[i / 2].x : h[i / 2].y;
     }
     return;
   }
 
   // ---- helper warps: rows 2 rp and 2 rp + 1 of a block, channels part kE .. + kE - 1; row br
   // of B and C, elements quarter kQ .. + kQ - 1
-  const int ht = tid - 32 * C::kSW;
+  const int ht = tid - 32 * kSW;
   const int rp = ht / C::kParts, part = ht % C::kParts, br = ht >> 2, quarter = ht & 3;
   const int cl = part * kE;
   const int left = rp < kTB / 2 ? nch - cl : 0;      // channels of this thread in the tile
@@ -344,34 +336,50 @@ __global__ void __launch_bounds__(C::kThreads) kda_scan_prefill_kernel(const Sca
     skip[e] = (p.D != nullptr && e < left) ? p.D[cbase + cl + e] : 0.f;
 
   // Ask for a thread's rows of block b (zeros where there are none).  Without the vectors'
-  // alignment the elements go through registers.
-  const auto bring = [&](auto n_c, Raw* dst, const Raw* src, const void* base, int count) {
-    constexpr int kN = decltype(n_c)::value;
-    if constexpr (kVec) {
-      copy_async<kN * static_cast<int>(sizeof(Raw))>(smem_u32(dst), count > 0 ? src : base,
-                                                     count <= 0);
-    } else {
-      Vec<T, kN> v;
-      v.template load<false>(src, count);
-      v.template store<true>(dst);
-    }
-  };
-  using NE = std::integral_constant<int, kE>;
-  using NQ = std::integral_constant<int, kQ>;
+  // alignment the elements go through registers: all are read, then all are put down.
   const auto request = [&](int b) {
     if (b < nblk) {
       typename C::Raws& r = sm.raw[b % C::kRing];
       const int rest = len - b * kTB;      // rows from the block's first on
+      const int n_bc = br < rest ? left_bc : 0;
+      int n_row[2];
 #pragma unroll
-      for (int o = 0; o < 2; ++o) {
-        const int count = 2 * rp + o < rest ? left : 0;
-        bring(NE(), r.x[o][ht], X + o * p.xs, p.x, count);
-        bring(NE(), r.dt[o][ht], DT + o * p.ds, p.dt, count);
-        if (gated) bring(NE(), r.z[o][ht], Z + o * p.zs, p.z, count);
+      for (int o = 0; o < 2; ++o) n_row[o] = 2 * rp + o < rest ? left : 0;
+      if constexpr (kVec) {
+        constexpr int kRow = kE * C::kElem, kBc = kQ * C::kElem;
+        const auto bring = [&](auto size, const Raw* dst, const Raw* src, const void* base, int n) {
+          copy_async<decltype(size)::value>(smem_u32(dst), n > 0 ? src : base, n <= 0);
+        };
+        const std::integral_constant<int, kRow> row{};
+        const std::integral_constant<int, kBc> bc{};
+#pragma unroll
+        for (int o = 0; o < 2; ++o) {
+          bring(row, r.x[o][ht], X + o * p.xs, p.x, n_row[o]);
+          bring(row, r.dt[o][ht], DT + o * p.ds, p.dt, n_row[o]);
+          if (gated) bring(row, r.z[o][ht], Z + o * p.zs, p.z, n_row[o]);
+        }
+        bring(bc, r.b[ht], Bp, p.B, n_bc);
+        bring(bc, r.c[ht], Cp, p.Cm, n_bc);
+      } else {
+        Vec<T, kE> vx[2], vd[2], vz[2];
+        Vec<T, kQ> vb, vc;
+#pragma unroll
+        for (int o = 0; o < 2; ++o) {
+          vx[o].template load<false>(X + o * p.xs, n_row[o]);
+          vd[o].template load<false>(DT + o * p.ds, n_row[o]);
+          if (gated) vz[o].template load<false>(Z + o * p.zs, n_row[o]);
+        }
+        vb.template load<false>(Bp, n_bc);
+        vc.template load<false>(Cp, n_bc);
+#pragma unroll
+        for (int o = 0; o < 2; ++o) {
+          vx[o].template store<true>(r.x[o][ht]);
+          vd[o].template store<true>(r.dt[o][ht]);
+          if (gated) vz[o].template store<true>(r.z[o][ht]);
+        }
+        vb.template store<true>(r.b[ht]);
+        vc.template store<true>(r.c[ht]);
       }
-      const int count = br < rest ? left_bc : 0;
-      bring(NQ(), r.b[ht], Bp, p.B, count);
-      bring(NQ(), r.c[ht], Cp, p.Cm, count);
       X += kTB * p.xs;
       DT += kTB * p.ds;
       Z += kTB * p.zs;
@@ -410,16 +418,10 @@ __global__ void __launch_bounds__(C::kThreads) kda_scan_prefill_kernel(const Sca
     vb.template load<true>(raw.b[ht]);
     vc.template load<true>(raw.c[ht]);
     uint32_t w[kWords];
-    if constexpr (kHalf == 0) {     // one element of 16 bits each: B low, C high
 #pragma unroll
-      for (int i = 0; i < kWords; ++i)
-        w[i] = __byte_perm(vb.w[i / 2], vc.w[i / 2], i % 2 ? 0x7632 : 0x5410);
-    } else {
-#pragma unroll
-      for (int i = 0; i < kWords / 2; ++i) {
-        w[i / kHalf * C::kLW + i % kHalf] = vb.w[i];
-        w[i / kHalf * C::kLW + kHalf + i % kHalf] = vc.w[i];
-      }
+    for (int i = 0; i < kWords / 2; ++i) {
+      w[i / kHalf * C::kLW + i % kHalf] = vb.w[i];
+      w[i / kHalf * C::kLW + kHalf + i % kHalf] = vc.w[i];
     }
     uint4* to = reinterpret_cast<uint4*>(&st.bc[br][quarter * kWords]);
 #pragma unroll
@@ -429,7 +431,18 @@ __global__ void __launch_bounds__(C::kThreads) kda_scan_prefill_kernel(const Sca
   const auto finish = [&](int b) {
     const typename C::Raws& raw = sm.raw[b % C::kRing];
     const int rest = len - b * kTB - 2 * rp;
-    if (left > 0) {
+    if (left > 0 && rest > 0) {
+      float2 sum[kE];      // of both rows
+#pragma unroll
+      for (int e = 0; e < kE; ++e) {
+#pragma unroll
+        for (int l = 0; l < C::kL / 2; ++l) {
+          const float4 v = *reinterpret_cast<const float4*>(
+              &sm.y[b & 1].part[rp][l][C::kParts * e + part][0]);
+          const float2 w = add2<true>(make_float2(v.x, v.y), make_float2(v.z, v.w));
+          sum[e] = l == 0 ? w : add2<true>(sum[e], w);
+        }
+      }
 #pragma unroll
       for (int o = 0; o < 2; ++o) {
         if (o >= rest) break;
@@ -438,8 +451,7 @@ __global__ void __launch_bounds__(C::kThreads) kda_scan_prefill_kernel(const Sca
         v.template load<true>(raw.x[o][ht]);
         v.unpack(xf);
 #pragma unroll
-        for (int e = 0; e < kE; ++e)
-          y[e] = fmaf(skip[e], xf[e], sm.y[b & 1][2 * rp + o][C::kParts * e + part]);
+        for (int e = 0; e < kE; ++e) y[e] = fmaf(skip[e], xf[e], o ? sum[e].y : sum[e].x);
         if (gated) {
           v.template load<true>(raw.z[o][ht]);
           v.unpack(zf);
@@ -666,20 +678,21 @@ bool go_prefill(ScanParams p, cudaStream_t s) {
       cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, kSmem) !=
           cudaSuccess)
     return false;
-  kernel<<<static_cast<unsigned>(grid), C::kThreads, kSmem, s>>>(p);
+  kernel<<<static_cast<unsigned>(grid), kThreads, kSmem, s>>>(p);
   return true;
 }
 
 template <typename T>
 bool launch_prefill(const ScanParams& p, int sms, cudaStream_t s) {
-  if (p.size > 64) return go_prefill<T, Cfg<T, 128, 8, 1, 4>>(p, s);
-  if (p.size > 32) return go_prefill<T, Cfg<T, 64, 8, 1, 4>>(p, s);
-  if (p.size > 16) return go_prefill<T, Cfg<T, 32, 4, 1, 4>>(p, s);
-  const int64_t chains = static_cast<int64_t>(p.seq.num) * p.channels;
-  if (chains < 8LL * sms) return go_prefill<T, Cfg<T, 16, 1, 1, 4>>(p, s);
-  if (chains < 16LL * sms) return go_prefill<T, Cfg<T, 16, 2, 1, 4>>(p, s);
-  if (chains < 64LL * sms) return go_prefill<T, Cfg<T, 16, 4, 1, 4>>(p, s);
-  return go_prefill<T, Cfg<T, 16, 4, 2, 4>>(p, s);
+  if (p.size > 64) return go_prefill<T, Cfg<T, 128, 8>>(p, s);
+  if (p.size > 32) return go_prefill<T, Cfg<T, 64, 8>>(p, s);
+  if (p.size > 16) return go_prefill<T, Cfg<T, 32, 4>>(p, s);
+  // Two elements per lane (16 channels a CTA) while that leaves no SM two CTAs, else four (32
+  // channels).  4096 rows of 1024 / 2048 / 2560 channels, us: two 119 / 121 / 198, four 154 /
+  // 159 / 159.
+  if (static_cast<int64_t>(p.seq.num) * p.channels <= 16LL * sms)
+    return go_prefill<T, Cfg<T, 16, 2>>(p, s);
+  return go_prefill<T, Cfg<T, 16, 4>>(p, s);
 }
 
 template <typename T, int kL>
