@@ -275,8 +275,8 @@ kda_conv_prefill_kernel(const ConvParams p, int32_t cols, int32_t groups) {
 }
 
 // kSeqs sequences at a time, so that their state rows and first new rows are all on their way
-// before any is used.
-template <typename T, int W, bool kVec, int kSeqs>
+// before any is used.  kOne: one new row each and no step states.
+template <typename T, int W, bool kVec, int kSeqs, bool kOne>
 __global__ void __launch_bounds__(256) kda_conv_decode_kernel(const ConvParams p, int32_t cols) {
   constexpr int kV = Cfg<T>::kV;
   using Raw = typename T::Raw;
@@ -285,7 +285,7 @@ __global__ void __launch_bounds__(256) kda_conv_decode_kernel(const ConvParams p
   const int c0 = (col * blockDim.x + threadIdx.x) * kV;
   if (c0 >= p.C) return;
   const int count = kVec ? kV : p.C - c0;
-  const int32_t T_new = p.seq.fixed_len;
+  const int32_t T_new = kOne ? 1 : p.seq.fixed_len;
   const int64_t row_c = static_cast<int64_t>(p.C);
   int32_t slot[kSeqs];
   Vec<T, kV> win[kSeqs][W];
@@ -326,7 +326,7 @@ __global__ void __launch_bounds__(256) kda_conv_decode_kernel(const ConvParams p
       out.put(row0 + t, y);
 #pragma unroll
       for (int j = 0; j < W - 1; ++j) win[i][j] = win[i][j + 1];
-      if (p.steps != nullptr) {
+      if (!kOne && p.steps != nullptr) {
         Raw* sp = static_cast<Raw*>(p.steps) + (row0 + t) * ((W - 1) * row_c) + c0;
 #pragma unroll
         for (int j = 0; j < W - 1; ++j) win[i][j].template store<kVec>(sp + j * row_c, count);
@@ -364,10 +364,11 @@ template <typename T>
 bool launch_prefill(ConvParams p, int W, int sms, cudaStream_t s) {
   const Shape sh = columns(p.C, Cfg<T>::kV);
   p.strips = (p.seq.rows + kStrip - 1) / kStrip;
-  // Adjacent strips share the weights and the W - 1 rows between them; a CTA walks two
-  // while that still leaves every SM several CTAs.
+  // Adjacent strips share the weights and the W - 1 rows between them; a CTA walks
+  // four while that still leaves every SM many CTAs (one, two, four of 29K rows of 4608
+  // channels: 117.6, 109.1, 105.3 us).
   p.strips_per_cta =
-      static_cast<int64_t>(p.strips) * sh.cols >= 16LL * sms ? 2 : 1;
+      static_cast<int64_t>(p.strips) * sh.cols >= 32LL * sms ? 4 : 1;
   const int64_t groups = (p.strips + p.strips_per_cta - 1) / p.strips_per_cta;
   const int64_t grid = (groups + p.seq.num) * sh.cols;
   if (grid > INT32_MAX) return false;
@@ -381,24 +382,31 @@ bool launch_prefill(ConvParams p, int W, int sms, cudaStream_t s) {
   return true;
 }
 
-template <typename T, int W, int kSeqs>
+template <typename T, int W, int kSeqs, bool kOne>
 bool go_decode(const ConvParams& p, const Shape& sh, cudaStream_t s) {
   const int64_t grid = static_cast<int64_t>((p.seq.num + kSeqs - 1) / kSeqs) * sh.cols;
   if (grid > INT32_MAX) return false;
-  const auto kernel =
-      p.vec ? kda_conv_decode_kernel<T, W, true, kSeqs> : kda_conv_decode_kernel<T, W, false, kSeqs>;
+  const auto kernel = p.vec ? kda_conv_decode_kernel<T, W, true, kSeqs, kOne>
+                            : kda_conv_decode_kernel<T, W, false, kSeqs, kOne>;
   kernel<<<static_cast<unsigned>(grid), sh.threads, 0, s>>>(p, sh.cols);
   return true;
 }
 
+template <typename T, int W>
+bool pick_decode(const ConvParams& p, int sms, cudaStream_t s) {
+  const Shape sh = columns(p.C, Cfg<T>::kV);
+  const bool one = p.seq.fixed_len == 1 && p.steps == nullptr;
+  // Two sequences per thread once the batch fills the SMs without that.
+  if (static_cast<int64_t>(p.seq.num) * sh.cols >= 8LL * sms)
+    return one ? go_decode<T, W, 2, true>(p, sh, s) : go_decode<T, W, 2, false>(p, sh, s);
+  return one ? go_decode<T, W, 1, true>(p, sh, s) : go_decode<T, W, 1, false>(p, sh, s);
+}
+
 template <typename T>
 bool launch_decode(const ConvParams& p, int W, int sms, cudaStream_t s) {
-  const Shape sh = columns(p.C, Cfg<T>::kV);
-  // Two sequences per thread once the batch fills the SMs without that.
-  const bool many = static_cast<int64_t>(p.seq.num) * sh.cols >= 8LL * sms;
-  if (W == 2) return many ? go_decode<T, 2, 2>(p, sh, s) : go_decode<T, 2, 1>(p, sh, s);
-  if (W == 3) return many ? go_decode<T, 3, 2>(p, sh, s) : go_decode<T, 3, 1>(p, sh, s);
-  return many ? go_decode<T, 4, 2>(p, sh, s) : go_decode<T, 4, 1>(p, sh, s);
+  if (W == 2) return pick_decode<T, 2>(p, sms, s);
+  if (W == 3) return pick_decode<T, 3>(p, sms, s);
+  return pick_decode<T, 4>(p, sms, s);
 }
 
 }  // namespace conv

@@ -229,6 +229,7 @@ struct ScanParams {
   int64_t xs, ds, zs, bs, cs;   // row strides
   int32_t channels, size, groups, per_group, tiles_per_group, pool;
   int32_t softplus, keep;
+  int32_t seqs_per_cta;         // decode: a multiple of 4
 };
 
 struct NormParams {

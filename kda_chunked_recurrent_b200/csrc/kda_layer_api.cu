@@ -14,7 +14,7 @@ namespace layer {
 bool launch_conv_prefill(const ConvParams& p, int W, int dtype, int sms, cudaStream_t s);
 bool launch_conv_decode(const ConvParams& p, int W, int dtype, int sms, cudaStream_t s);
 bool launch_scan_prefill(const ScanParams& p, int dtype, int sms, cudaStream_t s);
-bool launch_scan_decode(const ScanParams& p, int dtype, cudaStream_t s);
+bool launch_scan_decode(const ScanParams& p, int dtype, int sms, cudaStream_t s);
 bool launch_norm(const NormParams& p, int dtype, cudaStream_t s);
 }  // namespace layer
 }  // namespace kda
@@ -247,7 +247,7 @@ kda_status_t scan_call(const void* x, const void* dt, const float* A_log, const 
   p.keep = (flags & KDA_LAYER_KEEP_STATE) != 0;
   cudaStream_t s = static_cast<cudaStream_t>(stream);
   return launch(decode ? "kda_scan_decode" : "kda_scan_prefill", [&] {
-    return decode ? launch_scan_decode(p, sh->dtype, s)
+    return decode ? launch_scan_decode(p, sh->dtype, sms, s)
                   : launch_scan_prefill(p, sh->dtype, sms, s);
   });
 }

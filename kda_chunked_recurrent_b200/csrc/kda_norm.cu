@@ -53,182 +53,223 @@ __device__ __forceinline__ float row_reduce(float v, float* smem, int row_in_cta
   return v;
 }
 
-// kVec: the width is a multiple of 8 and all rows may be moved 16 bytes at a time.
-template <typename T, int kTPR, int kChunks, int kThreads, bool kVec>
+// kVec: the width is a multiple of 8 and all rows may be moved 16 bytes at a time.  kR rows
+// per thread: short rows share the weights and the reckoning of addresses.
+template <typename T, int kTPR, int kChunks, int kThreads, int kR, bool kVec>
 __global__ void __launch_bounds__(kThreads) kda_rms_norm_kernel(const NormParams p) {
   using Raw = typename T::Raw;
   static_assert(kThreads % kTPR == 0 && kTPR % 16 == 0, "whole rows and scale groups");
+  static_assert(kR == 1 || kTPR <= 32, "one row per thread where warps share it");
   __shared__ float s_sum[kThreads / 32], s_max[kThreads / 32];
-  constexpr int kRows = kThreads / kTPR;
+  constexpr int kRows = kThreads / kTPR;     // rows side by side; the CTA has kR times as many
   const int j = threadIdx.x % kTPR, ric = threadIdx.x / kTPR;
   const int W = p.width;
-  // token and head of the row: one division for the CTA's first row, where heads allow it
-  const int64_t first = static_cast<int64_t>(blockIdx.x) * kRows, row = first + ric;
-  int64_t tok = row;
-  int32_t head = 0;
+  const int64_t first = static_cast<int64_t>(blockIdx.x) * (kRows * kR);
+  // token and head of the CTA's first row; other rows are a few heads on
+  int64_t tok0 = first;
+  int32_t head0 = 0;
   if (p.heads > 1) {
-    const bool small = first <= UINT32_MAX;
-    tok = small ? static_cast<uint32_t>(first) / static_cast<uint32_t>(p.heads) : first / p.heads;
-    head = static_cast<int32_t>(first - tok * p.heads) + ric;
-    if (p.heads >= kRows) {
-      if (head >= p.heads) {
-        head -= p.heads;
-        ++tok;
+    tok0 = first <= UINT32_MAX ? static_cast<uint32_t>(first) / static_cast<uint32_t>(p.heads)
+                               : first / p.heads;
+    head0 = static_cast<int32_t>(first - tok0 * p.heads);
+  }
+  const int n0 = W - kE * j;                  // elements from the thread's first to the row's end
+  int64_t tok[kR];
+  int32_t at[kR];                             // the thread's first element within its token
+  int n[kR];
+#pragma unroll
+  for (int r = 0; r < kR; ++r) {
+    const int rr = r * kRows + ric;
+    n[r] = first + rr < p.rows ? n0 : 0;
+    tok[r] = tok0 + rr;
+    at[r] = kE * j;
+    if (p.heads > 1) {
+      int32_t head = head0 + rr;
+      tok[r] = tok0;
+      if (p.heads >= kRows * kR) {
+        if (head >= p.heads) {
+          head -= p.heads;
+          ++tok[r];
+        }
+      } else {
+        const int32_t over = head / p.heads;
+        tok[r] += over;
+        head -= over * p.heads;
       }
-    } else {
-      const int32_t over = head / p.heads;
-      tok += over;
-      head -= over * p.heads;
+      at[r] += head * W;
     }
   }
-  const int32_t at = head * W + kE * j;      // first element of the thread, within its token
-  int n = row < p.rows ? W - kE * j : 0;     // elements from there to the end of the row
-  const auto left = [&](int i) { return n - kE * i * kTPR; };
-
-  const auto load = [&](Vec<T, kE> (&v)[kChunks], const void* base, int64_t stride) {
-    const Raw* q = static_cast<const Raw*>(base) + tok * stride + at;
+  const auto left = [&](int r, int i) { return n[r] - kE * i * kTPR; };
+  const auto load = [&](Vec<T, kE> (&v)[kR][kChunks], const void* base, int64_t stride) {
 #pragma unroll
-    for (int i = 0; i < kChunks; ++i) {
-      if (left(i) > 0) v[i].template load<kVec>(q + kE * i * kTPR, left(i));
-      else v[i].clear();
+    for (int r = 0; r < kR; ++r) {
+      const Raw* q = static_cast<const Raw*>(base) + tok[r] * stride + at[r];
+#pragma unroll
+      for (int i = 0; i < kChunks; ++i) {
+        if (left(r, i) > 0) v[r][i].template load<kVec>(q + kE * i * kTPR, left(r, i));
+        else v[r][i].clear();
+      }
     }
   };
   // the gate is loaded with x where registers allow, else once x and the residual are spent
   constexpr bool kGateEarly = kChunks <= 4;
-  Vec<T, kE> xv[kChunks], rv[kChunks], gv[kChunks];
+  Vec<T, kE> xv[kR][kChunks], rv[kR][kChunks], gv[kR][kChunks];
   load(xv, p.x, p.xs);
   if (p.res != nullptr) load(rv, p.res, p.rs);
   if (kGateEarly && p.gate != nullptr) load(gv, p.gate, p.gs);
-  float2 y[kChunks][kE / 2];
-  float2 sq = make_float2(0.f, 0.f);
+  float2 y[kR][kChunks][kE / 2];
+  float sum[kR];
 #pragma unroll
-  for (int i = 0; i < kChunks; ++i) {
-    float f[kE];
-    xv[i].unpack(f);
+  for (int r = 0; r < kR; ++r) {
+    float2 sq = make_float2(0.f, 0.f);
 #pragma unroll
-    for (int e = 0; e < kE / 2; ++e) y[i][e] = make_float2(f[2 * e], f[2 * e + 1]);
-    if (p.res != nullptr) {
-      rv[i].unpack(f);
+    for (int i = 0; i < kChunks; ++i) {
+      float f[kE];
+      xv[r][i].unpack(f);
 #pragma unroll
-      for (int e = 0; e < kE / 2; ++e)
-        y[i][e] = add2<true>(y[i][e], make_float2(f[2 * e], f[2 * e + 1]));
+      for (int e = 0; e < kE / 2; ++e) y[r][i][e] = make_float2(f[2 * e], f[2 * e + 1]);
+      if (p.res != nullptr) {
+        rv[r][i].unpack(f);
+#pragma unroll
+        for (int e = 0; e < kE / 2; ++e)
+          y[r][i][e] = add2<true>(y[r][i][e], make_float2(f[2 * e], f[2 * e + 1]));
+      }
+#pragma unroll
+      for (int e = 0; e < kE / 2; ++e) sq = fma2<true>(y[r][i][e], y[r][i][e], sq);
     }
-#pragma unroll
-    for (int e = 0; e < kE / 2; ++e) sq = fma2<true>(y[i][e], y[i][e], sq);
+    sum[r] = sq.x + sq.y;
   }
   if (!kGateEarly && p.gate != nullptr) load(gv, p.gate, p.gs);
-  const auto packed = [&](int i) {
+  const auto packed = [&](int r, int i) {
     float f[kE];
 #pragma unroll
     for (int e = 0; e < kE / 2; ++e) {
-      f[2 * e] = y[i][e].x;
-      f[2 * e + 1] = y[i][e].y;
+      f[2 * e] = y[r][i][e].x;
+      f[2 * e + 1] = y[r][i][e].y;
     }
     Vec<T, kE> o;
     o.pack(f);
     return o;
   };
   if (p.res_out != nullptr) {
-    Raw* q = static_cast<Raw*>(p.res_out) + tok * p.ros + at;
 #pragma unroll
-    for (int i = 0; i < kChunks; ++i)
-      if (left(i) > 0) packed(i).template store<kVec>(q + kE * i * kTPR, left(i));
+    for (int r = 0; r < kR; ++r) {
+      Raw* q = static_cast<Raw*>(p.res_out) + tok[r] * p.ros + at[r];
+#pragma unroll
+      for (int i = 0; i < kChunks; ++i)
+        if (left(r, i) > 0) packed(r, i).template store<kVec>(q + kE * i * kTPR, left(r, i));
+    }
   }
-  const float sum = row_reduce<kTPR, kThreads, false>(sq.x + sq.y, s_sum, ric);
-  const float rstd = rsqrtf(fmaf(sum, p.inv_width, p.eps));
+  float rstd[kR];
+#pragma unroll
+  for (int r = 0; r < kR; ++r)
+    rstd[r] = rsqrtf(fmaf(row_reduce<kTPR, kThreads, false>(sum[r], s_sum, ric), p.inv_width, p.eps));
 
 #pragma unroll
   for (int i = 0; i < kChunks; ++i) {
+    float2 w[kE / 2];
     if (p.weight == nullptr) {
 #pragma unroll
-      for (int e = 0; e < kE / 2; ++e) y[i][e] = mul2<true>(y[i][e], make_float2(rstd, rstd));
+      for (int e = 0; e < kE / 2; ++e) w[e] = make_float2(1.f, 1.f);
     } else {
-      // (of a thread without a row too: its products are not written)
-      const int nw = W - kE * (j + i * kTPR);
+      const int nw = n0 - kE * i * kTPR;
       Vec<F32, kE> wv;
       if (nw > 0) wv.template load<kVec>(p.weight + kE * (j + i * kTPR), nw);
       else wv.clear();
 #pragma unroll
       for (int e = 0; e < kE / 2; ++e)
-        y[i][e] = mul2<true>(mul2<true>(y[i][e], make_float2(rstd, rstd)),
-                             make_float2(__uint_as_float(wv.w[2 * e]),
-                                         __uint_as_float(wv.w[2 * e + 1])));
+        w[e] = make_float2(__uint_as_float(wv.w[2 * e]), __uint_as_float(wv.w[2 * e + 1]));
     }
-    if (p.gate != nullptr) {
-      float g[kE];
-      gv[i].unpack(g);
 #pragma unroll
-      for (int e = 0; e < kE / 2; ++e) {
-        const float2 z = make_float2(g[2 * e], g[2 * e + 1]);
-        y[i][e] = mul2<true>(y[i][e], sigmoid2(z));
-        if (!p.sigmoid) y[i][e] = mul2<true>(y[i][e], z);
+    for (int r = 0; r < kR; ++r) {
+#pragma unroll
+      for (int e = 0; e < kE / 2; ++e)
+        y[r][i][e] = mul2<true>(mul2<true>(y[r][i][e], make_float2(rstd[r], rstd[r])), w[e]);
+      if (p.gate != nullptr) {
+        float g[kE];
+        gv[r][i].unpack(g);
+#pragma unroll
+        for (int e = 0; e < kE / 2; ++e) {
+          const float2 z = make_float2(g[2 * e], g[2 * e + 1]);
+          y[r][i][e] = mul2<true>(y[r][i][e], sigmoid2(z));
+          if (!p.sigmoid) y[r][i][e] = mul2<true>(y[r][i][e], z);
+        }
       }
     }
   }
 
   if (!p.out8) {
-    Raw* q = static_cast<Raw*>(p.out) + row * W + kE * j;
 #pragma unroll
-    for (int i = 0; i < kChunks; ++i)
-      if (left(i) > 0) packed(i).template store<kVec>(q + kE * i * kTPR, left(i));
+    for (int r = 0; r < kR; ++r) {
+      Raw* q = static_cast<Raw*>(p.out) + (first + r * kRows + ric) * W + kE * j;
+#pragma unroll
+      for (int i = 0; i < kChunks; ++i)
+        if (left(r, i) > 0) packed(r, i).template store<kVec>(q + kE * i * kTPR, left(r, i));
+    }
     return;
   }
 
   // 8 bits.  The scale and the factor 1 / scale are products with rounded constants and the
   // reciprocal approximation: within 2^-22 of the quotients.
-  const auto amax_of = [&](int i) {
-    float m = max_nan(fabsf(y[i][0].x), fabsf(y[i][0].y));
+  const auto amax_of = [&](int r, int i) {
+    float m = max_nan(fabsf(y[r][i][0].x), fabsf(y[r][i][0].y));
 #pragma unroll
-    for (int e = 1; e < kE / 2; ++e) m = max_nan(m, max_nan(fabsf(y[i][e].x), fabsf(y[i][e].y)));
+    for (int e = 1; e < kE / 2; ++e)
+      m = max_nan(m, max_nan(fabsf(y[r][i][e].x), fabsf(y[r][i][e].y)));
     return m;
   };
-  float factor[kChunks];
-  if (p.group == 0) {
-    float m = amax_of(0);
 #pragma unroll
-    for (int i = 1; i < kChunks; ++i) m = max_nan(m, amax_of(i));
-    const float amax = max_nan(row_reduce<kTPR, kThreads, true>(m, s_max, ric), kAmaxFloor);
-    if (n > 0 && j == 0) p.scales[row] = amax * (1.f / kE4m3Max);
+  for (int r = 0; r < kR; ++r) {
+    const int64_t row = first + r * kRows + ric;
+    float factor[kChunks];
+    if (p.group == 0) {
+      float m = amax_of(r, 0);
 #pragma unroll
-    for (int i = 0; i < kChunks; ++i) factor[i] = kE4m3Max * rcp_approx(amax);
-  } else {
+      for (int i = 1; i < kChunks; ++i) m = max_nan(m, amax_of(r, i));
+      const float amax = max_nan(row_reduce<kTPR, kThreads, true>(m, s_max, ric), kAmaxFloor);
+      if (n[r] > 0 && j == 0) p.scales[row] = amax * (1.f / kE4m3Max);
 #pragma unroll
-    for (int i = 0; i < kChunks; ++i) {
-      float m = amax_of(i);
-#pragma unroll
-      for (int o = 8; o > 0; o >>= 1) m = max_nan(m, __shfl_xor_sync(0xffffffffu, m, o));
-      const float amax = max_nan(m, kAmaxFloor);
-      if (left(i) > 0 && (j & 15) == 0)
-        p.scales[row * p.groups + (j + i * kTPR) / 16] = amax * (1.f / kE4m3Max);
-      factor[i] = kE4m3Max * rcp_approx(amax);
-    }
-  }
-  uint8_t* o = static_cast<uint8_t*>(p.out) + row * W + kE * j;
-#pragma unroll
-  for (int i = 0; i < kChunks; ++i) {
-    const float2 f = make_float2(factor[i], factor[i]);
-    uint32_t q[2];
-#pragma unroll
-    for (int h = 0; h < 2; ++h) {
-      const float2 a = mul2<true>(y[i][2 * h], f), b = mul2<true>(y[i][2 * h + 1], f);
-      q[h] = e4m3x2(a.x, a.y) | (e4m3x2(b.x, b.y) << 16);
-    }
-    if constexpr (kVec) {
-      if (left(i) > 0) *reinterpret_cast<uint2*>(o + kE * i * kTPR) = make_uint2(q[0], q[1]);
+      for (int i = 0; i < kChunks; ++i) factor[i] = kE4m3Max * rcp_approx(amax);
     } else {
 #pragma unroll
-      for (int e = 0; e < kE; ++e)
-        if (e < left(i)) o[kE * i * kTPR + e] = static_cast<uint8_t>(q[e / 4] >> (8 * (e % 4)));
+      for (int i = 0; i < kChunks; ++i) {
+        float m = amax_of(r, i);
+#pragma unroll
+        for (int o = 8; o > 0; o >>= 1) m = max_nan(m, __shfl_xor_sync(0xffffffffu, m, o));
+        const float amax = max_nan(m, kAmaxFloor);
+        if (left(r, i) > 0 && (j & 15) == 0)
+          p.scales[row * p.groups + (j + i * kTPR) / 16] = amax * (1.f / kE4m3Max);
+        factor[i] = kE4m3Max * rcp_approx(amax);
+      }
+    }
+    uint8_t* o = static_cast<uint8_t*>(p.out) + row * W + kE * j;
+#pragma unroll
+    for (int i = 0; i < kChunks; ++i) {
+      const float2 f = make_float2(factor[i], factor[i]);
+      uint32_t q[2];
+#pragma unroll
+      for (int h = 0; h < 2; ++h) {
+        const float2 a = mul2<true>(y[r][i][2 * h], f), b = mul2<true>(y[r][i][2 * h + 1], f);
+        q[h] = e4m3x2(a.x, a.y) | (e4m3x2(b.x, b.y) << 16);
+      }
+      if constexpr (kVec) {
+        if (left(r, i) > 0) *reinterpret_cast<uint2*>(o + kE * i * kTPR) = make_uint2(q[0], q[1]);
+      } else {
+#pragma unroll
+        for (int e = 0; e < kE; ++e)
+          if (e < left(r, i))
+            o[kE * i * kTPR + e] = static_cast<uint8_t>(q[e / 4] >> (8 * (e % 4)));
+      }
     }
   }
 }
 
-template <typename T, int kTPR, int kChunks, int kThreads>
+template <typename T, int kTPR, int kChunks, int kThreads, int kR = 1>
 bool go(const NormParams& p, cudaStream_t s) {
-  const int64_t per = kThreads / kTPR, grid = (p.rows + per - 1) / per;
+  const int64_t per = kThreads / kTPR * kR, grid = (p.rows + per - 1) / per;
   if (grid > INT32_MAX) return false;
-  const auto kernel = p.vec ? kda_rms_norm_kernel<T, kTPR, kChunks, kThreads, true>
-                            : kda_rms_norm_kernel<T, kTPR, kChunks, kThreads, false>;
+  const auto kernel = p.vec ? kda_rms_norm_kernel<T, kTPR, kChunks, kThreads, kR, true>
+                            : kda_rms_norm_kernel<T, kTPR, kChunks, kThreads, kR, false>;
   kernel<<<static_cast<unsigned>(grid), kThreads, 0, s>>>(p);
   return true;
 }
@@ -237,8 +278,8 @@ template <typename T>
 bool launch(const NormParams& p, cudaStream_t s) {
   // The fewest threads whose registers hold the row in few chunks each.
   const int W = p.width;
-  if (W <= 128) return go<T, 16, 1, 128>(p, s);
-  if (W <= 256) return go<T, 32, 1, 128>(p, s);
+  if (W <= 128) return go<T, 16, 1, 128, 4>(p, s);
+  if (W <= 256) return go<T, 32, 1, 128, 2>(p, s);
   if (W <= 512) return go<T, 32, 2, 128>(p, s);
   if (W <= 1024) return go<T, 128, 1, 128>(p, s);
   if (W <= 2048) return go<T, 128, 2, 128>(p, s);

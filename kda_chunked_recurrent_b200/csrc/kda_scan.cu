@@ -57,6 +57,15 @@ __device__ __forceinline__ void copy_wait() {
   asm volatile("cp.async.wait_group %0;" ::"n"(kPending) : "memory");
 }
 
+// e^v with the rounding of v log2(e) made good: the product's error times ln 2 is added to the
+// result relatively, so that a decay rate is off by no more than the exponential's own 2^-22.
+__device__ __forceinline__ float ex2_full(float v) {
+  const float y = v * kLog2e;
+  const float e = fmaf(v, kLog2e, -y) + v * 1.925963033500948e-8f;   // log2(e) - its FP32 value
+  const float r = ex2(y);
+  return fmaf(r, e * 0.6931471805599453f, r);
+}
+
 // log(1 + e^v) = max(v, 0) + log(1 + e), e = e^-|v| in (0, 1], with the logarithm from the
 // series of the inverse hyperbolic tangent, log(1 + e) = 2 atanh(s), s = e / (2 + e) <= 1/3,
 // which is relatively exact for a small e too (a step of 1e-3 is the usual case, and its
@@ -288,7 +297,7 @@ __global__ void __launch_bounds__(kThreads, 2) kda_scan_prefill_kernel(const Sca
     for (int i = 0; i < C::kS; ++i) {
       const bool in = ch < nch && q * C::kS + i < p.size;
       // elements past the state's size decay at rate 0 and take nothing: B and C are 0 there
-      A[i] = in ? -expf(p.A_log[at + i]) * kLog2e : 0.f;
+      A[i] = in ? -kLog2e * ex2_full(p.A_log[at + i]) : 0.f;
       const float v = (in && old) ? state[i] : 0.f;
       if (i % 2 == 0) h[i / 2].x = v;
       else h[i / 2].y = v;
@@ -494,8 +503,9 @@ __global__ void __launch_bounds__(kThreads, 2) kda_scan_prefill_kernel(const Sca
 // A lane's first duty is one of the four sequences: it alone loads dt, x and z there and takes
 // the softplus and the gate, and hands them to the other lanes of the channel; and it is left
 // with the sum of that sequence after the exchange.
-template <typename T, int kL, bool kVec>
-__global__ void __launch_bounds__(256, sizeof(typename T::Raw) == 4 ? 2 : 3)
+// kOne: one new token each and no step states.
+template <typename T, int kL, bool kVec, bool kOne>
+__global__ void __launch_bounds__(256, (sizeof(typename T::Raw) == 4 ? 2 : 3) + kOne)
 kda_scan_decode_kernel(const ScanParams p) {
   using Raw = typename T::Raw;
   constexpr int kCh = 256 / kL;     // channels per CTA
@@ -503,65 +513,15 @@ kda_scan_decode_kernel(const ScanParams p) {
   const int q = threadIdx.x % kL, cl = threadIdx.x / kL, own = q & 3;
   const int tiles = p.tiles_per_group;                 // channel tiles (groups may share one)
   const int tile = blockIdx.x % tiles;
-  const int32_t n0 = static_cast<int32_t>(blockIdx.x / tiles) * kN;
   const int ch = tile * kCh + cl;
   const bool on = ch < p.channels;
   const int c = on ? ch : p.channels - 1;              // idle threads follow the last channel
   const int e0 = 4 * q, count = on ? p.size - e0 : 0;  // state elements of this thread
-  const int32_t T_new = p.seq.fixed_len;
-  int32_t slot[kN];
-#pragma unroll
-  for (int s = 0; s < kN; ++s)
-    slot[s] = n0 + s < p.seq.num ? state_slot(p.slot, n0 + s, p.pool, p.status,
-                                              tile == 0 && threadIdx.x == 0)
-                                 : -1;
+  const int32_t T_new = kOne ? 1 : p.seq.fixed_len;
   const int64_t state_at = static_cast<int64_t>(c) * p.size + e0;
   const int64_t state_slot_size = static_cast<int64_t>(p.channels) * p.size;
-  Vec<F32, 4> sv[kN];
-#pragma unroll
-  for (int s = 0; s < kN; ++s) {
-    if (slot[s] >= 0 && count > 0)
-      sv[s].template load<kVec>(p.state + slot[s] * state_slot_size + state_at, count);
-    else
-      sv[s].clear();
-  }
-  // rows of token 0; token t is t strides on
-  const int64_t r_own = static_cast<int64_t>(n0 + own) * T_new;
-  const bool own_in = n0 + own < p.seq.num;
-  const bool own_live = own_in && (own == 0 ? slot[0] : own == 1 ? slot[1] : own == 2 ? slot[2]
-                                                                                      : slot[3]) >= 0;
-  const Raw* X = static_cast<const Raw*>(p.x) + r_own * p.xs + c;
-  const Raw* DT = static_cast<const Raw*>(p.dt) + r_own * p.ds + c;
-  const Raw* Z = static_cast<const Raw*>(p.z) + r_own * p.zs + c;
-  Raw* out = static_cast<Raw*>(p.out) + r_own * p.channels + c;
   const int64_t bc_at = static_cast<int64_t>(c / p.per_group) * p.size + e0;
-  const Raw* Bp = static_cast<const Raw*>(p.B) + static_cast<int64_t>(n0) * T_new * p.bs + bc_at;
-  const Raw* Cp = static_cast<const Raw*>(p.Cm) + static_cast<int64_t>(n0) * T_new * p.cs + bc_at;
-  struct Row {
-    Raw x, dt, z;
-    Vec<T, 4> b[kN], c[kN];
-  };
-  const auto fetch = [&](Row& r, int32_t t) {
-    if (own_live) {
-      r.x = X[t * p.xs];
-      r.dt = DT[t * p.ds];
-      if (p.z != nullptr) r.z = Z[t * p.zs];
-    } else {
-      r.x = r.dt = r.z = Raw(0);
-    }
-#pragma unroll
-    for (int s = 0; s < kN; ++s) {
-      if (slot[s] >= 0 && count > 0) {
-        r.b[s].template load<kVec>(Bp + (static_cast<int64_t>(s) * T_new + t) * p.bs, count);
-        r.c[s].template load<kVec>(Cp + (static_cast<int64_t>(s) * T_new + t) * p.cs, count);
-      } else {
-        r.b[s].clear();
-        r.c[s].clear();
-      }
-    }
-  };
-  Row cur;
-  fetch(cur, 0);
+  const int64_t b_seq = T_new * p.bs, c_seq = T_new * p.cs;   // from a sequence to the next
   float2 A[2];
   {
     Vec<F32, 4> av;
@@ -570,86 +530,145 @@ kda_scan_decode_kernel(const ScanParams p) {
     float a[4];
     av.unpack(a);
 #pragma unroll
-    for (int i = 0; i < 4; ++i) a[i] = i < count ? -expf(a[i]) * kLog2e : 0.f;
+    for (int i = 0; i < 4; ++i) a[i] = i < count ? -kLog2e * ex2_full(a[i]) : 0.f;
     A[0] = make_float2(a[0], a[1]);
     A[1] = make_float2(a[2], a[3]);
   }
   const float bias = p.dt_bias != nullptr ? p.dt_bias[c] : 0.f;
   const float skip = p.D != nullptr ? p.D[c] : 0.f;
-  float2 h[kN][2];
-#pragma unroll
-  for (int s = 0; s < kN; ++s) {
-    h[s][0] = make_float2(__uint_as_float(sv[s].w[0]), __uint_as_float(sv[s].w[1]));
-    h[s][1] = make_float2(__uint_as_float(sv[s].w[2]), __uint_as_float(sv[s].w[3]));
-  }
-  const auto pack_state = [&](int s) {
-    sv[s].w[0] = __float_as_uint(h[s][0].x);
-    sv[s].w[1] = __float_as_uint(h[s][0].y);
-    sv[s].w[2] = __float_as_uint(h[s][1].x);
-    sv[s].w[3] = __float_as_uint(h[s][1].y);
-  };
-  for (int32_t t = 0; t < T_new; ++t) {
-    const float x = T::to(cur.x);
-    float d = T::to(cur.dt) + bias;
-    if (p.softplus) d = softplus(d);
-    const float dx = d * x;
-    float part[kN];
-#pragma unroll
-    for (int s = 0; s < kN; ++s) {
-      // from the lane of this channel whose duty is sequence s
-      const int src = (threadIdx.x & 28) | s;
-      const float ds = __shfl_sync(0xffffffffu, d, src), dxs = __shfl_sync(0xffffffffu, dx, src);
-      float bf[4], cf[4];
-      cur.b[s].unpack(bf);
-      cur.c[s].unpack(cf);
-      float2 acc;
-#pragma unroll
-      for (int i = 0; i < 2; ++i) {
-        const float2 e = mul2<true>(make_float2(ds, ds), A[i]);
-        h[s][i] = fma2<true>(make_float2(ex2(e.x), ex2(e.y)), h[s][i],
-                             mul2<true>(make_float2(dxs, dxs),
-                                        make_float2(bf[2 * i], bf[2 * i + 1])));
-        const float2 cv = make_float2(cf[2 * i], cf[2 * i + 1]);
-        acc = i == 0 ? mul2<true>(cv, h[s][0]) : fma2<true>(cv, h[s][1], acc);
-      }
-      part[s] = acc.x + acc.y;
-    }
-    // four lanes exchange four sums, each keeps its own; then the other lanes of the channel
-    const bool b0 = own & 1, b1 = own & 2;
-    const float p0 = (b0 ? part[1] : part[0]) +
-                     __shfl_xor_sync(0xffffffffu, b0 ? part[0] : part[1], 1);
-    const float p1 = (b0 ? part[3] : part[2]) +
-                     __shfl_xor_sync(0xffffffffu, b0 ? part[2] : part[3], 1);
-    float y = (b1 ? p1 : p0) + __shfl_xor_sync(0xffffffffu, b1 ? p0 : p1, 2);
-#pragma unroll
-    for (int o = 4; o < kL; o <<= 1) y += __shfl_xor_sync(0xffffffffu, y, o);
-    y = fmaf(skip, x, y);
-    if (p.z != nullptr) {
-      const float z = T::to(cur.z);
-      y *= z * sigmoid(z);
-    }
-    // a padding row's output is zero
-    if (on && q < 4 && own_in)
-      out[static_cast<int64_t>(t) * p.channels] = T::from(own_live ? y : 0.f);
-    if (t + 1 < T_new) fetch(cur, t + 1);
-    if (p.steps != nullptr && count > 0) {
-#pragma unroll
-      for (int s = 0; s < kN; ++s)
-        if (slot[s] >= 0) {
-          pack_state(s);
-          sv[s].template store<kVec>(
-              p.steps + (static_cast<int64_t>(n0 + s) * T_new + t) * state_slot_size + state_at,
-              count);
-        }
-    }
-  }
-  if (!p.keep && count > 0) {
+  const int32_t first = static_cast<int32_t>(blockIdx.x / tiles) * p.seqs_per_cta;
+  const int32_t last = min(first + p.seqs_per_cta, p.seq.num);
+
+  for (int32_t n0 = first; n0 < last; n0 += kN) {
+    int32_t slot[kN];
 #pragma unroll
     for (int s = 0; s < kN; ++s)
-      if (slot[s] >= 0) {
-        pack_state(s);
-        sv[s].template store<kVec>(p.state + slot[s] * state_slot_size + state_at, count);
+      slot[s] = n0 + s < p.seq.num ? state_slot(p.slot, n0 + s, p.pool, p.status,
+                                                tile == 0 && threadIdx.x == 0)
+                                   : -1;
+    float2 h[kN][2];
+    const auto state_of = [&](int s) { return p.state + slot[s] * state_slot_size + state_at; };
+#pragma unroll
+    for (int s = 0; s < kN; ++s) {
+      Vec<F32, 4> v;
+      if (slot[s] >= 0 && count > 0) v.template load<kVec>(state_of(s), count);
+      else v.clear();
+      h[s][0] = make_float2(__uint_as_float(v.w[0]), __uint_as_float(v.w[1]));
+      h[s][1] = make_float2(__uint_as_float(v.w[2]), __uint_as_float(v.w[3]));
+    }
+    const auto put_state = [&](int s, float* to) {
+      Vec<F32, 4> v;
+      v.w[0] = __float_as_uint(h[s][0].x);
+      v.w[1] = __float_as_uint(h[s][0].y);
+      v.w[2] = __float_as_uint(h[s][1].x);
+      v.w[3] = __float_as_uint(h[s][1].y);
+      v.template store<kVec>(to, count);
+    };
+    // rows of token 0; token t is t strides on
+    const int64_t r_own = static_cast<int64_t>(n0 + own) * T_new;
+    const int64_t r_first = static_cast<int64_t>(n0) * T_new;
+    const bool own_in = n0 + own < p.seq.num;
+    const bool own_live = own_in && (own == 0   ? slot[0]
+                                     : own == 1 ? slot[1]
+                                     : own == 2 ? slot[2]
+                                                : slot[3]) >= 0;
+    const Raw* X = static_cast<const Raw*>(p.x) + r_own * p.xs + c;
+    const Raw* DT = static_cast<const Raw*>(p.dt) + r_own * p.ds + c;
+    const Raw* Z = static_cast<const Raw*>(p.z) + r_own * p.zs + c;
+    Raw* out = static_cast<Raw*>(p.out) + r_own * p.channels + c;
+    const Raw* Bp = static_cast<const Raw*>(p.B) + r_first * p.bs + bc_at;
+    const Raw* Cp = static_cast<const Raw*>(p.Cm) + r_first * p.cs + bc_at;
+    struct Row {
+      Raw x, dt, z;
+      Vec<T, 4> b[kN], c[kN];
+    };
+    const auto fetch = [&](Row& r) {       // the rows of the next token
+      r.x = r.dt = r.z = Raw(0);
+      if (own_live) {
+        r.x = *X;
+        r.dt = *DT;
+        if (p.z != nullptr) r.z = *Z;
       }
+      const Raw *bs = Bp, *cs = Cp;
+#pragma unroll
+      for (int s = 0; s < kN; ++s) {
+        if (slot[s] >= 0 && count > 0) {
+          r.b[s].template load<kVec>(bs, count);
+          r.c[s].template load<kVec>(cs, count);
+        } else {
+          r.b[s].clear();
+          r.c[s].clear();
+        }
+        bs += b_seq;
+        cs += c_seq;
+      }
+      if constexpr (!kOne) {
+        X += p.xs;
+        DT += p.ds;
+        Z += p.zs;
+        Bp += p.bs;
+        Cp += p.cs;
+      }
+    };
+    Row cur;
+    fetch(cur);
+    for (int32_t t = 0; t < T_new; ++t) {
+      const float x = T::to(cur.x);
+      float d = T::to(cur.dt) + bias;
+      if (p.softplus) d = softplus(d);
+      const float dx = d * x;
+      float part[kN];
+#pragma unroll
+      for (int s = 0; s < kN; ++s) {
+        // from the lane of this channel whose duty is sequence s
+        const int src = (threadIdx.x & 28) | s;
+        const float ds = __shfl_sync(0xffffffffu, d, src), dxs = __shfl_sync(0xffffffffu, dx, src);
+        float bf[4], cf[4];
+        cur.b[s].unpack(bf);
+        cur.c[s].unpack(cf);
+        float2 acc;
+#pragma unroll
+        for (int i = 0; i < 2; ++i) {
+          const float2 e = mul2<true>(splat(ds), A[i]);
+          h[s][i] = fma2<true>(make_float2(ex2(e.x), ex2(e.y)), h[s][i],
+                               mul2<true>(splat(dxs), make_float2(bf[2 * i], bf[2 * i + 1])));
+          const float2 cv = make_float2(cf[2 * i], cf[2 * i + 1]);
+          acc = i == 0 ? mul2<true>(cv, h[s][0]) : fma2<true>(cv, h[s][1], acc);
+        }
+        part[s] = acc.x + acc.y;
+      }
+      // four lanes exchange four sums, each keeps its own; then the other lanes of the channel
+      const bool b0 = own & 1, b1 = own & 2;
+      const float p0 = (b0 ? part[1] : part[0]) +
+                       __shfl_xor_sync(0xffffffffu, b0 ? part[0] : part[1], 1);
+      const float p1 = (b0 ? part[3] : part[2]) +
+                       __shfl_xor_sync(0xffffffffu, b0 ? part[2] : part[3], 1);
+      float y = (b1 ? p1 : p0) + __shfl_xor_sync(0xffffffffu, b1 ? p0 : p1, 2);
+#pragma unroll
+      for (int o = 4; o < kL; o <<= 1) y += __shfl_xor_sync(0xffffffffu, y, o);
+      y = fmaf(skip, x, y);
+      if (p.z != nullptr) {
+        const float z = T::to(cur.z);
+        y *= z * sigmoid(z);
+      }
+      // a padding row's output is zero
+      if (on && q < 4 && own_in) *out = T::from(own_live ? y : 0.f);
+      if constexpr (!kOne) {
+        out += p.channels;
+        if (t + 1 < T_new) fetch(cur);
+        if (p.steps != nullptr && count > 0) {
+#pragma unroll
+          for (int s = 0; s < kN; ++s)
+            if (slot[s] >= 0)
+              put_state(s, p.steps + ((r_first + s * T_new + t) * state_slot_size + state_at));
+        }
+      }
+    }
+    if (!p.keep && count > 0) {
+#pragma unroll
+      for (int s = 0; s < kN; ++s)
+        if (slot[s] >= 0) put_state(s, state_of(s));
+    }
   }
 }
 
@@ -696,24 +715,31 @@ bool launch_prefill(const ScanParams& p, int sms, cudaStream_t s) {
 }
 
 template <typename T, int kL>
-bool go_decode(ScanParams p, cudaStream_t s) {
+bool go_decode(ScanParams p, int sms, cudaStream_t s) {
   constexpr int kCh = 256 / kL, kN = 4, e = sizeof(typename T::Raw);
   p.tiles_per_group = (p.channels + kCh - 1) / kCh;
   const bool vec = p.size % 4 == 0 && whole(p.B, p.bs * e, 4 * e) && whole(p.Cm, p.cs * e, 4 * e) &&
                    whole(p.A_log, 0, 16);
-  const int64_t grid = static_cast<int64_t>((p.seq.num + kN - 1) / kN) * p.tiles_per_group;
+  // More sequences per CTA share its A once the batch fills the SMs many times without that.
+  p.seqs_per_cta = static_cast<int64_t>(p.seq.num) * p.tiles_per_group >= 64LL * sms ? 2 * kN : kN;
+  const int64_t grid = static_cast<int64_t>((p.seq.num + p.seqs_per_cta - 1) / p.seqs_per_cta) *
+                       p.tiles_per_group;
   if (grid > INT32_MAX) return false;
-  const auto kernel = vec ? kda_scan_decode_kernel<T, kL, true> : kda_scan_decode_kernel<T, kL, false>;
+  const bool one = p.seq.fixed_len == 1 && p.steps == nullptr;
+  const auto kernel = vec ? (one ? kda_scan_decode_kernel<T, kL, true, true>
+                                 : kda_scan_decode_kernel<T, kL, true, false>)
+                          : (one ? kda_scan_decode_kernel<T, kL, false, true>
+                                 : kda_scan_decode_kernel<T, kL, false, false>);
   kernel<<<static_cast<unsigned>(grid), 256, 0, s>>>(p);
   return true;
 }
 
 template <typename T>
-bool launch_decode(const ScanParams& p, cudaStream_t s) {
-  if (p.size > 64) return go_decode<T, 32>(p, s);
-  if (p.size > 32) return go_decode<T, 16>(p, s);
-  if (p.size > 16) return go_decode<T, 8>(p, s);
-  return go_decode<T, 4>(p, s);
+bool launch_decode(const ScanParams& p, int sms, cudaStream_t s) {
+  if (p.size > 64) return go_decode<T, 32>(p, sms, s);
+  if (p.size > 32) return go_decode<T, 16>(p, sms, s);
+  if (p.size > 16) return go_decode<T, 8>(p, sms, s);
+  return go_decode<T, 4>(p, sms, s);
 }
 
 }  // namespace scan
@@ -723,10 +749,10 @@ bool launch_scan_prefill(const ScanParams& p, int dtype, int sms, cudaStream_t s
   if (dtype == 1) return scan::launch_prefill<F16>(p, sms, s);
   return scan::launch_prefill<F32>(p, sms, s);
 }
-bool launch_scan_decode(const ScanParams& p, int dtype, cudaStream_t s) {
-  if (dtype == 0) return scan::launch_decode<Bf16>(p, s);
-  if (dtype == 1) return scan::launch_decode<F16>(p, s);
-  return scan::launch_decode<F32>(p, s);
+bool launch_scan_decode(const ScanParams& p, int dtype, int sms, cudaStream_t s) {
+  if (dtype == 0) return scan::launch_decode<Bf16>(p, sms, s);
+  if (dtype == 1) return scan::launch_decode<F16>(p, sms, s);
+  return scan::launch_decode<F32>(p, sms, s);
 }
 
 }  // namespace layer
