@@ -27,61 +27,57 @@ namespace conv {
 
 constexpr int kStrip = 8;
 
-template <typename T>
-struct Cfg {
-  static constexpr int kV = 4;   // channels per thread: 8 bytes of a 16-bit row, 16 of FP32
-};
-
 // kVec: every row, the weights and the outputs may be read and written 16 bytes at a time
 // (then a thread's channels lie in one part); else element by element.
-template <typename T, int W, bool kVec>
+template <bool kVec>
+struct Cfg {
+  // channels per thread: 8 bytes of a 16-bit row, 16 of FP32 (16 bytes of a 16-bit row took
+  // registers that loads in flight need: 157 against 135 us for 29K rows of 4608)
+  static constexpr int kV = kVec ? 4 : 1;
+};
+
+template <int W, bool kVec>
 struct Taps {
-  static constexpr int kV = Cfg<T>::kV;
-  float2 w[W][kV / 2];      // tap j of channel pairs
-  float2 bias[kV / 2];
+  static constexpr int kV = Cfg<kVec>::kV;
+  float w[W][kV];      // tap j of the thread's channels
+  float bias[kV];
 
   __device__ __forceinline__ void load(const ConvParams& p, int c0) {
-    float f[kV * W], g[kV];
-    if constexpr (kVec) {
-      Vec<F32, kV * W> wv;
-      wv.template load<true>(p.weight + static_cast<int64_t>(c0) * W);
-      wv.unpack(f);
-    }
-    const int n = min(kV, p.C - c0);
+    Vec<F32, kV * W> wv;
+    wv.template load<kVec>(p.weight + static_cast<int64_t>(c0) * W);
 #pragma unroll
     for (int i = 0; i < kV; ++i) {
-      if constexpr (!kVec) {
 #pragma unroll
-        for (int j = 0; j < W; ++j)
-          f[i * W + j] = i < n ? p.weight[static_cast<int64_t>(c0 + i) * W + j] : 0.f;
-      }
-      g[i] = (p.bias != nullptr && i < n) ? p.bias[c0 + i] : 0.f;
-    }
-#pragma unroll
-    for (int i = 0; i < kV / 2; ++i) {
-#pragma unroll
-      for (int j = 0; j < W; ++j) w[j][i] = make_float2(f[2 * i * W + j], f[(2 * i + 1) * W + j]);
-      bias[i] = make_float2(g[2 * i], g[2 * i + 1]);
+      for (int j = 0; j < W; ++j) w[j][i] = __uint_as_float(wv.w[i * W + j]);
+      bias[i] = p.bias != nullptr ? p.bias[c0 + i] : 0.f;
     }
   }
   // u: the W window rows, oldest first
   __device__ __forceinline__ void apply(const float (&u)[W][kV], bool act, float (&y)[kV]) const {
-    float2 a[kV / 2];
+    if constexpr (kV == 1) {
+      float a = bias[0];
 #pragma unroll
-    for (int i = 0; i < kV / 2; ++i) {
-      a[i] = bias[i];
+      for (int j = 0; j < W; ++j) a = fmaf(w[j][0], u[j][0], a);
+      y[0] = act ? a * sigmoid(a) : a;
+    } else {
+float2 a[kV / 2];
 #pragma unroll
-      for (int j = 0; j < W; ++j)
-        a[i] = fma2<true>(w[j][i], make_float2(u[j][2 * i], u[j][2 * i + 1]), a[i]);
-    }
-    if (act) {
+      for (int i = 0; i < kV / 2; ++i) {
+        a[i] = make_float2(bias[2 * i], bias[2 * i + 1]);
 #pragma unroll
-      for (int i = 0; i < kV / 2; ++i) a[i] = silu2(a[i]);
-    }
+        for (int j = 0; j < W; ++j)
+          a[i] = fma2<true>(make_float2(w[j][2 * i], w[j][2 * i + 1]),
+                            make_float2(u[j][2 * i], u[j][2 * i + 1]), a[i]);
+      }
+      if (act) {
 #pragma unroll
-    for (int i = 0; i < kV / 2; ++i) {
-      y[2 * i] = a[i].x;
-      y[2 * i + 1] = a[i].y;
+        for (int i = 0; i < kV / 2; ++i) a[i] = silu2(a[i]);
+      }
+#pragma unroll
+      for (int i = 0; i < kV / 2; ++i) {
+        y[2 * i] = a[i].x;
+        y[2 * i + 1] = a[i].y;
+      }
     }
   }
 };
@@ -89,27 +85,19 @@ struct Taps {
 // Where a thread's channels go: parts are contiguous blocks of all rows.
 template <typename T, bool kVec>
 struct Out {
-  static constexpr int kV = Cfg<T>::kV;
+  static constexpr int kV = Cfg<kVec>::kV;
   using Raw = typename T::Raw;
-  Raw* base;   // channel c0 of row 0
-  const ConvParams& p;
-  int c0;
-  __device__ __forceinline__ Out(const ConvParams& p_, int c) : p(p_), c0(c) { base = at(c); }
-  __device__ __forceinline__ Raw* at(int c) const {
+  Raw* base;   // the thread's first channel of row 0
+  int32_t part_c;
+  __device__ __forceinline__ Out(const ConvParams& p, int c) : part_c(p.part_c) {
     const int part = c / p.part_c;
-    return static_cast<Raw*>(p.out) + static_cast<int64_t>(part) * p.seq.rows * p.part_c +
+    base = static_cast<Raw*>(p.out) + static_cast<int64_t>(part) * p.seq.rows * p.part_c +
            (c - part * p.part_c);
   }
   __device__ __forceinline__ void put(int64_t row, const float (&y)[kV]) const {
-    if constexpr (kVec) {
-      Vec<T, kV> r;
-      r.pack(y);
-      r.template store<true>(base + row * p.part_c);
-    } else {
-#pragma unroll
-      for (int i = 0; i < kV; ++i)
-        if (c0 + i < p.C) at(c0 + i)[row * p.part_c] = T::from(y[i]);
-    }
+    Vec<T, kV> r;
+    r.pack(y);
+    r.template store<kVec>(base + row * part_c);
   }
 };
 
@@ -131,10 +119,9 @@ __device__ __forceinline__ int32_t find_seq(const Seqs& s, int32_t t) {
 
 template <typename T, int W, bool kVec>
 __device__ __forceinline__ void strips_body(const ConvParams& p, int group, int c0) {
-  constexpr int kV = Cfg<T>::kV;
+  constexpr int kV = Cfg<kVec>::kV;
   using Raw = typename T::Raw;
   const bool on = c0 < p.C;
-  const int count = p.C - c0;
   const int32_t rows = p.seq.rows;
   int32_t t0 = group * p.strips_per_cta * kStrip;     // rows < 2^31 - 4096
   const int32_t t_end = min(rows, t0 + p.strips_per_cta * kStrip);
@@ -145,18 +132,18 @@ __device__ __forceinline__ void strips_body(const ConvParams& p, int group, int 
   const auto fetch = [&](auto from) {
     if (on && t0 >= W - 1 && t0 + kStrip <= rows) {
 #pragma unroll
-      for (int i = decltype(from)::value; i < W - 1 + kStrip; ++i) r[i].template load<kVec>(px + i * xs, count);
+      for (int i = decltype(from)::value; i < W - 1 + kStrip; ++i) r[i].template load<kVec>(px + i * xs);
     } else {
 #pragma unroll
       for (int i = decltype(from)::value; i < W - 1 + kStrip; ++i) {
         const int32_t t = t0 - (W - 1) + i;
-        if (on && t >= 0 && t < rows) r[i].template load<kVec>(px + i * xs, count);
+        if (on && t >= 0 && t < rows) r[i].template load<kVec>(px + i * xs);
         else r[i].clear();
       }
     }
   };
   fetch(std::integral_constant<int, 0>());
-  Taps<T, W, kVec> taps;
+  Taps<W, kVec> taps;
   if (on) taps.load(p, c0);
   const Out<T, kVec> out(p, on ? c0 : 0);
   int32_t n = find_seq(p.seq, t0), a, b;
@@ -202,10 +189,9 @@ __device__ __forceinline__ void strips_body(const ConvParams& p, int group, int 
 // The first W - 1 rows of sequence n and the state that it leaves.
 template <typename T, int W, bool kVec>
 __device__ __forceinline__ void head_body(const ConvParams& p, int32_t n, int c0) {
-  constexpr int kV = Cfg<T>::kV;
+  constexpr int kV = Cfg<kVec>::kV;
   using Raw = typename T::Raw;
   if (c0 >= p.C) return;
-  const int count = kVec ? kV : p.C - c0;
   int32_t a, b;
   p.seq.range(n, a, b);
   const int32_t len = b - a;
@@ -218,9 +204,9 @@ __device__ __forceinline__ void head_body(const ConvParams& p, int32_t n, int c0
   Vec<T, kV> past[W - 1], head[W - 1], tail[W - 1];
 #pragma unroll
   for (int j = 0; j < W - 1; ++j) {
-    if (old) past[j].template load<kVec>(st + static_cast<int64_t>(j) * p.C, count);
+    if (old) past[j].template load<kVec>(st + static_cast<int64_t>(j) * p.C);
     else past[j].clear();
-    if (j < len) head[j].template load<kVec>(x + static_cast<int64_t>(a + j) * p.x_stride, count);
+    if (j < len) head[j].template load<kVec>(x + static_cast<int64_t>(a + j) * p.x_stride);
     else head[j].clear();
   }
   if (slot >= 0) {
@@ -229,7 +215,7 @@ __device__ __forceinline__ void head_body(const ConvParams& p, int32_t n, int c0
     for (int j = 0; j < W - 1; ++j) {
       const int32_t r = len + j;
       if (r >= W - 1) {
-        tail[j].template load<kVec>(x + static_cast<int64_t>(a + r - (W - 1)) * p.x_stride, count);
+        tail[j].template load<kVec>(x + static_cast<int64_t>(a + r - (W - 1)) * p.x_stride);
       } else {
 #pragma unroll
         for (int k = 0; k < W - 1; ++k)
@@ -237,7 +223,7 @@ __device__ __forceinline__ void head_body(const ConvParams& p, int32_t n, int c0
       }
     }
   }
-  Taps<T, W, kVec> taps;
+  Taps<W, kVec> taps;
   taps.load(p, c0);
   const Out<T, kVec> out(p, c0);
   float u[2 * (W - 1)][kV];
@@ -260,7 +246,7 @@ __device__ __forceinline__ void head_body(const ConvParams& p, int32_t n, int c0
   if (slot >= 0) {
 #pragma unroll
     for (int j = 0; j < W - 1; ++j)
-      tail[j].template store<kVec>(st + static_cast<int64_t>(j) * p.C, count);
+      tail[j].template store<kVec>(st + static_cast<int64_t>(j) * p.C);
   }
 }
 
@@ -269,7 +255,7 @@ template <typename T, int W, bool kVec>
 __global__ void __launch_bounds__(256)
 kda_conv_prefill_kernel(const ConvParams p, int32_t cols, int32_t groups) {
   const int col = blockIdx.x % cols, i = blockIdx.x / cols;
-  const int c0 = (col * blockDim.x + threadIdx.x) * Cfg<T>::kV;
+  const int c0 = (col * blockDim.x + threadIdx.x) * Cfg<kVec>::kV;
   if (i < groups) strips_body<T, W, kVec>(p, i, c0);
   else head_body<T, W, kVec>(p, i - groups, c0);
 }
@@ -278,13 +264,12 @@ kda_conv_prefill_kernel(const ConvParams p, int32_t cols, int32_t groups) {
 // before any is used.  kOne: one new row each and no step states.
 template <typename T, int W, bool kVec, int kSeqs, bool kOne>
 __global__ void __launch_bounds__(256) kda_conv_decode_kernel(const ConvParams p, int32_t cols) {
-  constexpr int kV = Cfg<T>::kV;
+  constexpr int kV = Cfg<kVec>::kV;
   using Raw = typename T::Raw;
   const int col = blockIdx.x % cols;
   const int32_t n0 = static_cast<int32_t>(blockIdx.x / cols) * kSeqs;
   const int c0 = (col * blockDim.x + threadIdx.x) * kV;
   if (c0 >= p.C) return;
-  const int count = kVec ? kV : p.C - c0;
   const int32_t T_new = kOne ? 1 : p.seq.fixed_len;
   const int64_t row_c = static_cast<int64_t>(p.C);
   int32_t slot[kSeqs];
@@ -298,14 +283,14 @@ __global__ void __launch_bounds__(256) kda_conv_decode_kernel(const ConvParams p
     const Raw* st = static_cast<const Raw*>(p.state) + slot[i] * ((W - 1) * row_c) + c0;
 #pragma unroll
     for (int j = 0; j < W - 1; ++j)
-      if (slot[i] >= 0) win[i][j].template load<kVec>(st + j * row_c, count);
+      if (slot[i] >= 0) win[i][j].template load<kVec>(st + j * row_c);
       else win[i][j].clear();
     if (slot[i] >= 0)
-      win[i][W - 1].template load<kVec>(x + static_cast<int64_t>(n0 + i) * T_new * p.x_stride, count);
+      win[i][W - 1].template load<kVec>(x + static_cast<int64_t>(n0 + i) * T_new * p.x_stride);
     else
       win[i][W - 1].clear();
   }
-  Taps<T, W, kVec> taps;
+  Taps<W, kVec> taps;
   taps.load(p, c0);
   const Out<T, kVec> out(p, c0);
 #pragma unroll
@@ -318,7 +303,7 @@ __global__ void __launch_bounds__(256) kda_conv_decode_kernel(const ConvParams p
       continue;
     }
     for (int32_t t = 0; t < T_new; ++t) {
-      if (t > 0) win[i][W - 1].template load<kVec>(x + (row0 + t) * p.x_stride, count);
+      if (t > 0) win[i][W - 1].template load<kVec>(x + (row0 + t) * p.x_stride);
       float u[W][kV], y[kV];
 #pragma unroll
       for (int j = 0; j < W; ++j) win[i][j].unpack(u[j]);
@@ -329,13 +314,13 @@ __global__ void __launch_bounds__(256) kda_conv_decode_kernel(const ConvParams p
       if (!kOne && p.steps != nullptr) {
         Raw* sp = static_cast<Raw*>(p.steps) + (row0 + t) * ((W - 1) * row_c) + c0;
 #pragma unroll
-        for (int j = 0; j < W - 1; ++j) win[i][j].template store<kVec>(sp + j * row_c, count);
+        for (int j = 0; j < W - 1; ++j) win[i][j].template store<kVec>(sp + j * row_c);
       }
     }
     if (!p.keep) {
       Raw* st = static_cast<Raw*>(p.state) + slot[i] * ((W - 1) * row_c) + c0;
 #pragma unroll
-      for (int j = 0; j < W - 1; ++j) win[i][j].template store<kVec>(st + j * row_c, count);
+      for (int j = 0; j < W - 1; ++j) win[i][j].template store<kVec>(st + j * row_c);
     }
   }
 }
@@ -362,7 +347,7 @@ Shape columns(int32_t C, int v) {
 
 template <typename T>
 bool launch_prefill(ConvParams p, int W, int sms, cudaStream_t s) {
-  const Shape sh = columns(p.C, Cfg<T>::kV);
+  const Shape sh = columns(p.C, p.vec ? Cfg<true>::kV : Cfg<false>::kV);
   p.strips = (p.seq.rows + kStrip - 1) / kStrip;
   // Adjacent strips share the weights and the W - 1 rows between them; a CTA walks
   // four while that still leaves every SM many CTAs (one, two, four of 29K rows of 4608
@@ -394,7 +379,7 @@ bool go_decode(const ConvParams& p, const Shape& sh, cudaStream_t s) {
 
 template <typename T, int W>
 bool pick_decode(const ConvParams& p, int sms, cudaStream_t s) {
-  const Shape sh = columns(p.C, Cfg<T>::kV);
+  const Shape sh = columns(p.C, p.vec ? Cfg<true>::kV : Cfg<false>::kV);
   const bool one = p.seq.fixed_len == 1 && p.steps == nullptr;
   // Two sequences per thread once the batch fills the SMs without that.
   if (static_cast<int64_t>(p.seq.num) * sh.cols >= 8LL * sms)

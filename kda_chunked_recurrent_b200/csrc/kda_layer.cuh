@@ -117,6 +117,40 @@ struct Vec {
         }
     }
   }
+  // In pieces of kStep elements that lie whole within `count` or behind it (kStep = 1: any).
+  template <int kStep>
+  __device__ __forceinline__ void load_by(const typename T::Raw* p, int count) {
+    if constexpr (kStep == n) {
+      load<true>(p);
+    } else if constexpr (kStep == 1) {
+      load<false>(p, count);
+    } else {
+#pragma unroll
+      for (int i = 0; i < n / kStep; ++i) {
+        Vec<T, kStep> v;
+        if (i * kStep < count) v.template load<true>(p + i * kStep);
+        else v.clear();
+#pragma unroll
+        for (int k = 0; k < kWords * kStep / n; ++k) w[i * (kWords * kStep / n) + k] = v.w[k];
+      }
+    }
+  }
+  template <int kStep>
+  __device__ __forceinline__ void store_by(typename T::Raw* p, int count) const {
+    if constexpr (kStep == n) {
+      store<true>(p);
+    } else if constexpr (kStep == 1) {
+      store<false>(p, count);
+    } else {
+#pragma unroll
+      for (int i = 0; i < n / kStep; ++i) {
+        Vec<T, kStep> v;
+#pragma unroll
+        for (int k = 0; k < kWords * kStep / n; ++k) v.w[k] = w[i * (kWords * kStep / n) + k];
+        if (i * kStep < count) v.template store<true>(p + i * kStep);
+      }
+    }
+  }
   __device__ __forceinline__ void unpack(float (&f)[n]) const {
     if constexpr (sizeof(typename T::Raw) == 4) {
 #pragma unroll
@@ -240,7 +274,8 @@ struct NormParams {
   int64_t xs, rs, ros, gs;      // token strides
   int64_t rows;                 // tokens * heads
   int32_t heads, width, group, groups;
-  int32_t out8, sigmoid, vec;
+  int32_t out8, sigmoid;
+  int32_t step;                 // elements that may be moved at a time: 8, 4 or 1
   float eps, inv_width;
 };
 

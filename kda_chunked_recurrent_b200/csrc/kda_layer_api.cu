@@ -360,9 +360,16 @@ kda_status_t kda_rms_norm(const void* x, const float* weight, const void* residu
   p.groups = static_cast<int32_t>(groups);
   p.out8 = out8;
   p.sigmoid = (flags & KDA_NORM_GATE_SIGMOID) != 0;
-  p.vec = W % 8 == 0 && rows16(x, sh.x_stride, e) && rows16(residual, sh.residual_stride, e) &&
-          rows16(residual_out, sh.residual_out_stride, e) && rows16(gate, sh.gate_stride, e) &&
-          aligned(out, out8 ? 8 : 16) && aligned(weight, 16);
+  const auto rows_of = [&](int n) {      // n elements at a time everywhere
+    const int64_t a = n == 8 ? 16 : n * e;
+    const auto ok = [&](const void* q, int64_t stride) {
+      return q == nullptr || (aligned(q, a) && stride * e % a == 0);
+    };
+    return W % n == 0 && ok(x, sh.x_stride) && ok(residual, sh.residual_stride) &&
+           ok(residual_out, sh.residual_out_stride) && ok(gate, sh.gate_stride) &&
+           aligned(out, out8 ? n : a) && aligned(weight, 16);
+  };
+  p.step = rows_of(8) ? 8 : rows_of(4) ? 4 : 1;
   p.eps = sh.eps;
   p.inv_width = static_cast<float>(1.0 / static_cast<double>(W));
   cudaStream_t s = static_cast<cudaStream_t>(stream);

@@ -53,9 +53,10 @@ __device__ __forceinline__ float row_reduce(float v, float* smem, int row_in_cta
   return v;
 }
 
-// kVec: the width is a multiple of 8 and all rows may be moved 16 bytes at a time.  kR rows
-// per thread: short rows share the weights and the reckoning of addresses.
-template <typename T, int kTPR, int kChunks, int kThreads, int kR, bool kVec>
+// kStep: elements that are moved at a time: 8 (the width is a multiple of 8, all rows lie on 16
+// bytes), 4 (the same with 4 and half the bytes) or 1.  kR rows per thread: short rows share
+// the weights and the reckoning of addresses.
+template <typename T, int kTPR, int kChunks, int kThreads, int kR, int kStep>
 __global__ void __launch_bounds__(kThreads) kda_rms_norm_kernel(const NormParams p) {
   using Raw = typename T::Raw;
   static_assert(kThreads % kTPR == 0 && kTPR % 16 == 0, "whole rows and scale groups");
@@ -106,7 +107,7 @@ __global__ void __launch_bounds__(kThreads) kda_rms_norm_kernel(const NormParams
       const Raw* q = static_cast<const Raw*>(base) + tok[r] * stride + at[r];
 #pragma unroll
       for (int i = 0; i < kChunks; ++i) {
-        if (left(r, i) > 0) v[r][i].template load<kVec>(q + kE * i * kTPR, left(r, i));
+        if (left(r, i) > 0) v[r][i].template load_by<kStep>(q + kE * i * kTPR, left(r, i));
         else v[r][i].clear();
       }
     }
@@ -157,7 +158,7 @@ __global__ void __launch_bounds__(kThreads) kda_rms_norm_kernel(const NormParams
       Raw* q = static_cast<Raw*>(p.res_out) + tok[r] * p.ros + at[r];
 #pragma unroll
       for (int i = 0; i < kChunks; ++i)
-        if (left(r, i) > 0) packed(r, i).template store<kVec>(q + kE * i * kTPR, left(r, i));
+        if (left(r, i) > 0) packed(r, i).template store_by<kStep>(q + kE * i * kTPR, left(r, i));
     }
   }
   float rstd[kR];
@@ -174,7 +175,7 @@ __global__ void __launch_bounds__(kThreads) kda_rms_norm_kernel(const NormParams
     } else {
       const int nw = n0 - kE * i * kTPR;
       Vec<F32, kE> wv;
-      if (nw > 0) wv.template load<kVec>(p.weight + kE * (j + i * kTPR), nw);
+      if (nw > 0) wv.template load_by<kStep>(p.weight + kE * (j + i * kTPR), nw);
       else wv.clear();
 #pragma unroll
       for (int e = 0; e < kE / 2; ++e)
@@ -204,7 +205,7 @@ __global__ void __launch_bounds__(kThreads) kda_rms_norm_kernel(const NormParams
       Raw* q = static_cast<Raw*>(p.out) + (first + r * kRows + ric) * W + kE * j;
 #pragma unroll
       for (int i = 0; i < kChunks; ++i)
-        if (left(r, i) > 0) packed(r, i).template store<kVec>(q + kE * i * kTPR, left(r, i));
+        if (left(r, i) > 0) packed(r, i).template store_by<kStep>(q + kE * i * kTPR, left(r, i));
     }
     return;
   }
@@ -252,8 +253,11 @@ __global__ void __launch_bounds__(kThreads) kda_rms_norm_kernel(const NormParams
         const float2 a = mul2<true>(y[r][i][2 * h], f), b = mul2<true>(y[r][i][2 * h + 1], f);
         q[h] = e4m3x2(a.x, a.y) | (e4m3x2(b.x, b.y) << 16);
       }
-      if constexpr (kVec) {
+      if constexpr (kStep == 8) {
         if (left(r, i) > 0) *reinterpret_cast<uint2*>(o + kE * i * kTPR) = make_uint2(q[0], q[1]);
+      } else if constexpr (kStep == 4) {
+        if (left(r, i) > 0) *reinterpret_cast<uint32_t*>(o + kE * i * kTPR) = q[0];
+        if (left(r, i) > 4) *reinterpret_cast<uint32_t*>(o + kE * i * kTPR + 4) = q[1];
       } else {
 #pragma unroll
         for (int e = 0; e < kE; ++e)
@@ -268,8 +272,9 @@ template <typename T, int kTPR, int kChunks, int kThreads, int kR = 1>
 bool go(const NormParams& p, cudaStream_t s) {
   const int64_t per = kThreads / kTPR * kR, grid = (p.rows + per - 1) / per;
   if (grid > INT32_MAX) return false;
-  const auto kernel = p.vec ? kda_rms_norm_kernel<T, kTPR, kChunks, kThreads, kR, true>
-                            : kda_rms_norm_kernel<T, kTPR, kChunks, kThreads, kR, false>;
+  const auto kernel = p.step == 8   ? kda_rms_norm_kernel<T, kTPR, kChunks, kThreads, kR, 8>
+                      : p.step == 4 ? kda_rms_norm_kernel<T, kTPR, kChunks, kThreads, kR, 4>
+                                    : kda_rms_norm_kernel<T, kTPR, kChunks, kThreads, kR, 1>;
   kernel<<<static_cast<unsigned>(grid), kThreads, 0, s>>>(p);
   return true;
 }

@@ -345,7 +345,8 @@ __global__ void __launch_bounds__(kThreads, 2) kda_scan_prefill_kernel(const Sca
     skip[e] = (p.D != nullptr && e < left) ? p.D[cbase + cl + e] : 0.f;
 
   // Ask for a thread's rows of block b (zeros where there are none).  Without the vectors'
-  // alignment the elements go through registers: all are read, then all are put down.
+  // alignment the elements come one by one; 16-bit ones, which no asynchronous copy takes, go
+  // through registers: all are read, then all are put down.
   const auto request = [&](int b) {
     if (b < nblk) {
       typename C::Raws& r = sm.raw[b % C::kRing];
@@ -361,6 +362,22 @@ __global__ void __launch_bounds__(kThreads, 2) kda_scan_prefill_kernel(const Sca
         };
         const std::integral_constant<int, kRow> row{};
         const std::integral_constant<int, kBc> bc{};
+#pragma unroll
+        for (int o = 0; o < 2; ++o) {
+          bring(row, r.x[o][ht], X + o * p.xs, p.x, n_row[o]);
+          bring(row, r.dt[o][ht], DT + o * p.ds, p.dt, n_row[o]);
+          if (gated) bring(row, r.z[o][ht], Z + o * p.zs, p.z, n_row[o]);
+        }
+        bring(bc, r.b[ht], Bp, p.B, n_bc);
+        bring(bc, r.c[ht], Cp, p.Cm, n_bc);
+      } else if constexpr (C::kElem == 4) {
+        const auto bring = [&](auto size, const Raw* dst, const Raw* src, const void* base, int n) {
+#pragma unroll
+          for (int i = 0; i < decltype(size)::value; ++i)
+            copy_async<4>(smem_u32(dst + i), i < n ? src + i : base, i >= n);
+        };
+        const std::integral_constant<int, kE> row{};
+        const std::integral_constant<int, kQ> bc{};
 #pragma unroll
         for (int o = 0; o < 2; ++o) {
           bring(row, r.x[o][ht], X + o * p.xs, p.x, n_row[o]);
@@ -505,7 +522,7 @@ __global__ void __launch_bounds__(kThreads, 2) kda_scan_prefill_kernel(const Sca
 // with the sum of that sequence after the exchange.
 // kOne: one new token each and no step states.
 template <typename T, int kL, bool kVec, bool kOne>
-__global__ void __launch_bounds__(256, (sizeof(typename T::Raw) == 4 ? 2 : 3) + kOne)
+__global__ void __launch_bounds__(256, (kOne ? 3 : 1) + (sizeof(typename T::Raw) == 2))
 kda_scan_decode_kernel(const ScanParams p) {
   using Raw = typename T::Raw;
   constexpr int kCh = 256 / kL;     // channels per CTA
@@ -610,9 +627,10 @@ kda_scan_decode_kernel(const ScanParams p) {
         Cp += p.cs;
       }
     };
-    Row cur;
+    Row cur, next;
     fetch(cur);
     for (int32_t t = 0; t < T_new; ++t) {
+      if (!kOne && t + 1 < T_new) fetch(next);
       const float x = T::to(cur.x);
       float d = T::to(cur.dt) + bias;
       if (p.softplus) d = softplus(d);
@@ -655,7 +673,7 @@ kda_scan_decode_kernel(const ScanParams p) {
       if (on && q < 4 && own_in) *out = T::from(own_live ? y : 0.f);
       if constexpr (!kOne) {
         out += p.channels;
-        if (t + 1 < T_new) fetch(cur);
+        cur = next;
         if (p.steps != nullptr && count > 0) {
 #pragma unroll
           for (int s = 0; s < kN; ++s)
