@@ -13,7 +13,8 @@ namespace kda {
 namespace layer {
 bool launch_conv_prefill(const ConvParams& p, int W, int dtype, int sms, cudaStream_t s);
 bool launch_conv_decode(const ConvParams& p, int W, int dtype, int sms, cudaStream_t s);
-bool launch_scan_prefill(const ScanParams& p, int dtype, int sms, cudaStream_t s);
+bool launch_scan_prefill(const ScanParams& p, int64_t max_rows, int dtype, int sms,
+                         cudaStream_t s);
 bool launch_scan_decode(const ScanParams& p, int dtype, int sms, cudaStream_t s);
 bool launch_norm(const NormParams& p, int dtype, cudaStream_t s);
 }  // namespace layer
@@ -245,10 +246,14 @@ kda_status_t scan_call(const void* x, const void* dt, const float* A_log, const 
   p.pool = static_cast<int32_t>(P);
   p.softplus = (flags & KDA_SCAN_SOFTPLUS) != 0;
   p.keep = (flags & KDA_LAYER_KEEP_STATE) != 0;
+  // the longest sequence that there may be: without cu_seqlens known, else at most the hint
+  const int64_t max_rows = sa.cu == nullptr ? rows / N
+                           : sh->max_seqlen > 0 ? sh->max_seqlen
+                                                : rows;
   cudaStream_t s = static_cast<cudaStream_t>(stream);
   return launch(decode ? "kda_scan_decode" : "kda_scan_prefill", [&] {
     return decode ? launch_scan_decode(p, sh->dtype, sms, s)
-                  : launch_scan_prefill(p, sh->dtype, sms, s);
+                  : launch_scan_prefill(p, max_rows, sh->dtype, sms, s);
   });
 }
 

@@ -66,6 +66,18 @@ __device__ __forceinline__ float ex2_full(float v) {
   return fmaf(r, e * 0.6931471805599453f, r);
 }
 
+// All threads of a cluster: what was written before the arrival is seen after the wait.
+__device__ __forceinline__ void cluster_arrive() { asm volatile("barrier.cluster.arrive;" ::: "memory"); }
+__device__ __forceinline__ void cluster_wait() { asm volatile("barrier.cluster.wait;" ::: "memory"); }
+// A float of another CTA of the cluster, at the place of `p` in its shared memory.
+__device__ __forceinline__ float cluster_load(const float* p, int rank) {
+  float v;
+  uint32_t a;
+  asm volatile("mapa.shared::cluster.u32 %0, %1, %2;" : "=r"(a) : "r"(smem_u32(p)), "r"(rank));
+  asm volatile("ld.shared::cluster.f32 %0, [%1];" : "=f"(v) : "r"(a) : "memory");
+  return v;
+}
+
 // log(1 + e^v) = max(v, 0) + log(1 + e), e = e^-|v| in (0, 1], with the logarithm from the
 // series of the inverse hyperbolic tangent, log(1 + e) = 2 atanh(s), s = e / (2 + e) <= 1/3,
 // which is relatively exact for a small e too (a step of 1e-3 is the usual case, and its
@@ -130,7 +142,6 @@ struct Cfg {
     Stage st[2];
     Sums y[2];     // (16-byte aligned: what precedes is whole vectors)
   };
-  static_assert(sizeof(Smem) <= 227 * 1024, "shared memory of a CTA");
   static_assert(kCH % 8 == 0 && kL >= 4, "helper parts; pairs of lanes");
 };
 
@@ -210,10 +221,11 @@ __device__ __forceinline__ float run_row(const Ops<C>& o, float2 (&h)[Ops<C>::kP
 // are interleaved here: beside the recurrence of one step stand the exponentials of the next
 // and the shared-memory reads of the one after.  Rows from nt on have d = 0 and B = C = 0 and
 // change nothing.
-template <typename T, typename C>
+// kOut false: the state alone, and the sum of the steps d in `d_sum`.
+template <typename T, typename C, bool kOut>
 __device__ __forceinline__ void scan_block(const typename C::Stage& st, typename C::Sums& y,
                                            float2 (&h)[Ops<C>::kP], const float (&A)[C::kS],
-                                           int ch0, int q, int nt) {
+                                           float& d_sum, int ch0, int q, int nt) {
   Rows<T, C> r0, r1;
   Ops<C> o0, o1;
   r0.load(st, 0, ch0, q);
@@ -232,8 +244,14 @@ __device__ __forceinline__ void scan_block(const typename C::Stage& st, typename
     // The lane's parts of the sums as they are: the helper that writes the rows adds the kL
     // parts (cheaper than exchanging them between the scan's lanes).
 #pragma unroll
-    for (int u = 0; u < kU; u += 2)
-      y.part[(t + u) / 2][q / 2][ch0][q % 2] = make_float2(sum[u], sum[u + 1]);
+    for (int u = 0; u < kU; u += 2) {
+      if constexpr (kOut) {
+        y.part[(t + u) / 2][q / 2][ch0][q % 2] = make_float2(sum[u], sum[u + 1]);
+      } else {
+        const float4 dd = st.dd[(t + u) / 2][ch0];
+        d_sum += dd.x + dd.y;
+      }
+    }
   };
   for (int t = 0; t < nt; t += 2 * kU) {
     step(t, r0, r1, o1, o0);
@@ -241,8 +259,20 @@ __device__ __forceinline__ void scan_block(const typename C::Stage& st, typename
   }
 }
 
+// What the CTAs of a cluster tell one another: per scan lane, the state that its rows leave
+// when they start from zeros, and the sum of their steps.
+template <typename C>
+struct Exchange {
+  float h[32 * kSW][C::kS], d[32 * kSW];
+};
+
 // kVec: the rows' vectors may be moved whole (then a part is inside the tile or outside).
-template <typename T, typename C, bool kVec>
+// kSplit > 1: a cluster of kSplit CTAs shares the rows of one sequence and tile.  Each first
+// takes its run of rows from a zero state; over run j a state h becomes
+//   exp(A sum_j d) h + h_j,
+// so every CTA has the state before its run from its predecessors' h_j and sums, and takes the
+// run again with outputs.
+template <typename T, typename C, bool kVec, int kSplit>
 __global__ void __launch_bounds__(kThreads, 2) kda_scan_prefill_kernel(const ScanParams p) {
   using Raw = typename T::Raw;
   constexpr int kE = C::kE, kQ = C::kQ;
@@ -250,8 +280,9 @@ __global__ void __launch_bounds__(kThreads, 2) kda_scan_prefill_kernel(const Sca
   typename C::Smem& sm = *reinterpret_cast<typename C::Smem*>(smem_raw);
   const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
   const int tiles = p.groups * p.tiles_per_group;
-  int32_t n = blockIdx.x / tiles;
-  const int tile = blockIdx.x - n * tiles;
+  const int seg = blockIdx.x % kSplit, unit = blockIdx.x / kSplit;
+  int32_t n = unit / tiles;
+  const int tile = unit - n * tiles;
   // Ragged batches: the longest sequences first, so that the last CTAs to start are short.
   if (p.seq.cu != nullptr && p.seq.num > 1 && p.seq.num <= kThreads) {
     int32_t* lens = reinterpret_cast<int32_t*>(smem_raw);
@@ -279,10 +310,22 @@ __global__ void __launch_bounds__(kThreads, 2) kda_scan_prefill_kernel(const Sca
   const int nch = min(C::kCH, p.per_group - in_grp);         // channels in it
   int32_t row0, row1;
   p.seq.range(n, row0, row1);
+  const int32_t slot = p.state == nullptr ? -1
+                                          : state_slot(p.slot, n, p.pool, p.status,
+                                                       tile == 0 && seg == 0 && tid == 0);
+  bool leaves_state = slot >= 0;
+  if constexpr (kSplit > 1) {
+    // runs of whole blocks; the CTA of the last row (of the first run, without rows) leaves
+    // the state
+    const int32_t blocks = (row1 - row0 + kTB - 1) / kTB, per = (blocks + kSplit - 1) / kSplit;
+    leaves_state = leaves_state && seg == (blocks == 0 ? 0 : (blocks - 1) / per);
+    row0 = min(row0 + seg * per * kTB, row1);
+    row1 = min(row0 + per * kTB, row1);
+  } else if (row0 == row1 && slot < 0) {
+    return;
+  }
   const int32_t len = row1 - row0, nblk = (len + kTB - 1) / kTB;
-  const int32_t slot =
-      p.state == nullptr ? -1 : state_slot(p.slot, n, p.pool, p.status, tile == 0 && tid == 0);
-  if (len == 0 && slot < 0) return;
+  Exchange<C>& ex = *reinterpret_cast<Exchange<C>*>(smem_raw + sizeof(typename C::Smem));
 
   if (warp < kSW) {
     // ---- scan warps
@@ -302,16 +345,44 @@ __global__ void __launch_bounds__(kThreads, 2) kda_scan_prefill_kernel(const Sca
       if (i % 2 == 0) h[i / 2].x = v;
       else h[i / 2].y = v;
     }
-    __syncthreads();
-    for (int b = 0; b < nblk; ++b) {
-      scan_block<T, C>(sm.st[b & 1], sm.y[b & 1], h, A, ch0, q, min(kTB, len - b * kTB));
+    const auto run = [&](auto out, float2 (&hh)[Ops<C>::kP], float& d_sum) {
       __syncthreads();
+      for (int b = 0; b < nblk; ++b) {
+        scan_block<T, C, decltype(out)::value>(sm.st[b & 1], sm.y[b & 1], hh, A, d_sum, ch0, q,
+                                               min(kTB, len - b * kTB));
+        __syncthreads();
+      }
+    };
+    float d_sum = 0.f;
+    if constexpr (kSplit > 1) {
+      float2 hl[Ops<C>::kP];
+#pragma unroll
+      for (int i = 0; i < Ops<C>::kP; ++i) hl[i] = make_float2(0.f, 0.f);
+      run(std::false_type(), hl, d_sum);
+#pragma unroll
+      for (int i = 0; i < C::kS; ++i) ex.h[tid][i] = i % 2 == 0 ? hl[i / 2].x : hl[i / 2].y;
+      ex.d[tid] = d_sum;
+      cluster_arrive();
+      cluster_wait();
+      for (int j = 0; j < seg; ++j) {
+        const float d = cluster_load(&ex.d[tid], j);
+#pragma unroll
+        for (int i = 0; i < Ops<C>::kP; ++i) {
+          const float2 y = mul2<true>(splat(d), make_float2(A[2 * i], A[2 * i + 1]));
+          h[i] = fma2<true>(make_float2(ex2(y.x), ex2(y.y)), h[i],
+                            make_float2(cluster_load(&ex.h[tid][2 * i], j),
+                                        cluster_load(&ex.h[tid][2 * i + 1], j)));
+        }
+      }
+      cluster_arrive();     // the neighbours' shared memory is not looked at any more
     }
-    if (slot >= 0) {
+    run(std::true_type(), h, d_sum);
+    if (leaves_state) {
 #pragma unroll
       for (int i = 0; i < C::kS; ++i)
         if (ch < nch && q * C::kS + i < p.size) state[i] = i % 2 == 0 ? h[i / 2].x : h[i / 2].y;
     }
+    if constexpr (kSplit > 1) cluster_wait();
     return;
   }
 
@@ -328,11 +399,7 @@ __global__ void __launch_bounds__(kThreads, 2) kda_scan_prefill_kernel(const Sca
   };
   // rows of the block that is copied next
   const int64_t lrow = static_cast<int64_t>(row0) + 2 * rp, brow = static_cast<int64_t>(row0) + br;
-  const Raw* X = rows_at(p.x, p.xs, lrow, cbase + cl);
-  const Raw* DT = rows_at(p.dt, p.ds, lrow, cbase + cl);
-  const Raw* Z = rows_at(p.z, p.zs, lrow, cbase + cl);
-  const Raw* Bp = rows_at(p.B, p.bs, brow, static_cast<int64_t>(grp) * p.size + quarter * kQ);
-  const Raw* Cp = rows_at(p.Cm, p.cs, brow, static_cast<int64_t>(grp) * p.size + quarter * kQ);
+  const Raw *X = nullptr, *DT = nullptr, *Z = nullptr, *Bp = nullptr, *Cp = nullptr;
   // row of the block that is written next
   Raw* O = static_cast<Raw*>(p.out) + lrow * p.channels + cbase + cl;
   float2 bias[kE];
@@ -499,21 +566,37 @@ __global__ void __launch_bounds__(kThreads, 2) kda_scan_prefill_kernel(const Sca
   // b + kRing - 2 are there in turn b.  A thread reads back only what it copied itself: its
   // own wait is all the ordering that needs.
   constexpr int kPending = C::kRing - 3;
-  for (int b = 0; b < C::kRing - 2; ++b) request(b);
-  copy_wait<kPending>();
-  if (nblk > 0) stage(0);
-  __syncthreads();
-  // Turn b, beside the scan of block b: block b + kRing - 2 is asked for, block b + 1 staged,
-  // block b - 1 written.
-  for (int b = 0; b < nblk; ++b) {
-    request(b + C::kRing - 2);
+  const auto run = [&](auto out) {
+    constexpr bool kOut = decltype(out)::value;
+    X = rows_at(p.x, p.xs, lrow, cbase + cl);
+    DT = rows_at(p.dt, p.ds, lrow, cbase + cl);
+    Z = rows_at(p.z, p.zs, lrow, cbase + cl);
+    Bp = rows_at(p.B, p.bs, brow, static_cast<int64_t>(grp) * p.size + quarter * kQ);
+    Cp = rows_at(p.Cm, p.cs, brow, static_cast<int64_t>(grp) * p.size + quarter * kQ);
+    for (int b = 0; b < C::kRing - 2; ++b) request(b);
     copy_wait<kPending>();
-    if (b + 1 < nblk) stage(b + 1);
-    if (b > 0) finish(b - 1);
+    if (nblk > 0) stage(0);
     __syncthreads();
+    // Turn b, beside the scan of block b: block b + kRing - 2 is asked for, block b + 1 staged,
+    // block b - 1 written.
+    for (int b = 0; b < nblk; ++b) {
+      request(b + C::kRing - 2);
+      copy_wait<kPending>();
+      if (b + 1 < nblk) stage(b + 1);
+      if (kOut && b > 0) finish(b - 1);
+      __syncthreads();
+    }
+    copy_wait<0>();
+    if (kOut && nblk > 0) finish(nblk - 1);
+  };
+  if constexpr (kSplit > 1) {
+    run(std::false_type());
+    cluster_arrive();
+    cluster_wait();
+    cluster_arrive();
   }
-  copy_wait<0>();
-  if (nblk > 0) finish(nblk - 1);
+  run(std::true_type());
+  if constexpr (kSplit > 1) cluster_wait();
 }
 
 // ---- tokens: four elements per lane, kL lanes per channel, four sequences at a time.
@@ -697,7 +780,7 @@ bool whole(const void* q, int64_t stride_bytes, int bytes) {
   return q == nullptr || (reinterpret_cast<uintptr_t>(q) % a == 0 && stride_bytes % a == 0);
 }
 
-template <typename T, typename C>
+template <typename T, typename C, int kSplit>
 bool go_prefill(ScanParams p, cudaStream_t s) {
   p.tiles_per_group = (p.per_group + C::kCH - 1) / C::kCH;
   constexpr int e = sizeof(typename T::Raw), kRow = C::kE * e, kBc = C::kQ * e;
@@ -706,30 +789,59 @@ bool go_prefill(ScanParams p, cudaStream_t s) {
                    whole(p.out, static_cast<int64_t>(p.channels) * e, kRow) &&
                    p.per_group % C::kE == 0 && whole(p.B, p.bs * e, kBc) &&
                    whole(p.Cm, p.cs * e, kBc) && p.size % C::kQ == 0;
-  const int64_t grid = static_cast<int64_t>(p.seq.num) * p.groups * p.tiles_per_group;
+  const int64_t grid = static_cast<int64_t>(p.seq.num) * p.groups * p.tiles_per_group * kSplit;
   if (grid > INT32_MAX) return false;
-  constexpr int kSmem = sizeof(typename C::Smem);
-  const auto kernel =
-      vec ? kda_scan_prefill_kernel<T, C, true> : kda_scan_prefill_kernel<T, C, false>;
+  constexpr int kSmem = sizeof(typename C::Smem) + (kSplit > 1 ? sizeof(Exchange<C>) : 0);
+  static_assert(kSmem <= 227 * 1024, "shared memory of a CTA");
+  const auto kernel = vec ? kda_scan_prefill_kernel<T, C, true, kSplit>
+                          : kda_scan_prefill_kernel<T, C, false, kSplit>;
   if (kSmem > 48 * 1024 &&
       cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, kSmem) !=
           cudaSuccess)
     return false;
-  kernel<<<static_cast<unsigned>(grid), kThreads, kSmem, s>>>(p);
-  return true;
+  cudaLaunchConfig_t cfg{};
+  cfg.gridDim = dim3(static_cast<unsigned>(grid));
+  cfg.blockDim = dim3(kThreads);
+  cfg.dynamicSmemBytes = kSmem;
+  cfg.stream = s;
+  cudaLaunchAttribute cluster{};
+  cluster.id = cudaLaunchAttributeClusterDimension;
+  cluster.val.clusterDim.x = kSplit;
+  cluster.val.clusterDim.y = cluster.val.clusterDim.z = 1;
+  cfg.attrs = &cluster;
+  cfg.numAttrs = kSplit > 1 ? 1 : 0;
+  return cudaLaunchKernelEx(&cfg, kernel, p) == cudaSuccess;
+}
+
+// Few channels and many rows: the rows are shared by a cluster of 8 or 4 CTAs.  A run is taken
+// twice, so the time falls to a quarter or a half at best.  One sequence, 16-bit rows, us, by
+// one CTA / 4 / 8 (256 channels; 592; 1024):
+//    512 rows   18.2 / 12.5 / 12.5;   18.7 / 16.6 / 20.0
+//   2048 rows   57.6 / 31.0 / 26.9;   59.7 / 45.3 / 46.0
+//   4096 rows    110 / 55.6 / 45.3;                         119 / 88 / 94
+// and more channels than that fill the SMs without.
+template <typename T, typename C>
+bool pick_prefill(const ScanParams& p, int64_t max_rows, int sms, cudaStream_t s) {
+  const int64_t tiles = static_cast<int64_t>(p.seq.num) * p.groups *
+                        ((p.per_group + C::kCH - 1) / C::kCH);
+  if (max_rows >= 512) {
+    if (tiles * 32 <= 7LL * sms) return go_prefill<T, C, 8>(p, s);
+    if (tiles * 4 <= 2LL * sms) return go_prefill<T, C, 4>(p, s);
+  }
+  return go_prefill<T, C, 1>(p, s);
 }
 
 template <typename T>
-bool launch_prefill(const ScanParams& p, int sms, cudaStream_t s) {
-  if (p.size > 64) return go_prefill<T, Cfg<T, 128, 8>>(p, s);
-  if (p.size > 32) return go_prefill<T, Cfg<T, 64, 8>>(p, s);
-  if (p.size > 16) return go_prefill<T, Cfg<T, 32, 4>>(p, s);
+bool launch_prefill(const ScanParams& p, int64_t max_rows, int sms, cudaStream_t s) {
+  if (p.size > 64) return pick_prefill<T, Cfg<T, 128, 8>>(p, max_rows, sms, s);
+  if (p.size > 32) return pick_prefill<T, Cfg<T, 64, 8>>(p, max_rows, sms, s);
+  if (p.size > 16) return pick_prefill<T, Cfg<T, 32, 4>>(p, max_rows, sms, s);
   // Two elements per lane (16 channels a CTA) while that leaves no SM two CTAs, else four (32
   // channels).  4096 rows of 1024 / 2048 / 2560 channels, us: two 119 / 121 / 198, four 154 /
   // 159 / 159.
   if (static_cast<int64_t>(p.seq.num) * p.channels <= 16LL * sms)
-    return go_prefill<T, Cfg<T, 16, 2>>(p, s);
-  return go_prefill<T, Cfg<T, 16, 4>>(p, s);
+    return pick_prefill<T, Cfg<T, 16, 2>>(p, max_rows, sms, s);
+  return go_prefill<T, Cfg<T, 16, 4>, 1>(p, s);
 }
 
 template <typename T, int kL>
@@ -762,10 +874,11 @@ bool launch_decode(const ScanParams& p, int sms, cudaStream_t s) {
 
 }  // namespace scan
 
-bool launch_scan_prefill(const ScanParams& p, int dtype, int sms, cudaStream_t s) {
-  if (dtype == 0) return scan::launch_prefill<Bf16>(p, sms, s);
-  if (dtype == 1) return scan::launch_prefill<F16>(p, sms, s);
-  return scan::launch_prefill<F32>(p, sms, s);
+bool launch_scan_prefill(const ScanParams& p, int64_t max_rows, int dtype, int sms,
+                         cudaStream_t s) {
+  if (dtype == 0) return scan::launch_prefill<Bf16>(p, max_rows, sms, s);
+  if (dtype == 1) return scan::launch_prefill<F16>(p, max_rows, sms, s);
+  return scan::launch_prefill<F32>(p, max_rows, sms, s);
 }
 bool launch_scan_decode(const ScanParams& p, int dtype, int sms, cudaStream_t s) {
   if (dtype == 0) return scan::launch_decode<Bf16>(p, sms, s);

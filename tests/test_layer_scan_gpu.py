@@ -220,3 +220,31 @@ def test_nan_stays_in_its_sequence_and_channel():
     bad = ~torch.isfinite(y)
     assert bad[10:45, 3].all() and bad[60:90, 5].all()
     assert bad.sum() == 35 + 30
+
+
+# few channels and many rows: the rows of a sequence are shared by several thread blocks
+@pytest.mark.parametrize("dtype,D,S,G", [("bf16", 40, 16, 1), ("f32", 250, 13, 2), ("f16", 64, 64, 2),
+                                         ("f32", 24, 128, 1), ("bf16", 31, 20, 1)])
+@pytest.mark.parametrize("lens", [[512], [513, 0, 31], [1500, 7], [5, 33, 600, 256]])
+def test_prompts_few_channels_many_rows(dtype, D, S, G, lens):
+    _check_prefill(lens, D, S, G, dtype, extra=5, hint=False)
+
+
+@pytest.mark.parametrize("dtype", ["bf16", "f32"])
+@pytest.mark.parametrize("lens,D", [([600], 700), ([1030, 3], 560), ([700], 1184)])
+def test_prompts_some_channels_many_rows(dtype, lens, D):
+    _check_prefill(lens, D, 16, 1, dtype, hint=False)
+
+
+def test_prompts_few_channels_small_steps():
+    """Steps near 1e-4: what comes before a run of rows still matters at its end."""
+    import kda_chunked_recurrent_b200 as K
+    g = torch.Generator().manual_seed(9)
+    x, dt, A_log, B, C, Dv, z, _ = _inputs(2000, 32, 16, 1, "f32", g, sliced=False, gate=True)
+    dt = dt.abs() * 1e-4
+    pool = torch.randn(1, 32, 16, generator=g).cuda()
+    h0 = f64(pool[0])
+    out = K.scan_prefill(x, dt, A_log, B, C, D=Dv, z=z, state=pool, softplus=False)
+    y, yb, hs, es = scan(f64(x), f64(dt), f64(A_log), f64(B), f64(C), f64(Dv), f64(z), None, h0, False)
+    close(out, y, yb, torch.float32, "rows")
+    close(pool[0], hs[-1], es[-1], torch.float32, "state")
