@@ -263,7 +263,8 @@ struct ScanParams {
   int64_t xs, ds, zs, bs, cs;   // row strides
   int32_t channels, size, groups, per_group, tiles_per_group, pool;
   int32_t softplus, keep;
-  int32_t seqs_per_cta;         // decode: a multiple of 4
+  int32_t vec_bc;               // prompts: vectors of B and C may be moved whole
+  int32_t longest_first;        // prompts: CTAs take the sequences by falling length
 };
 
 struct NormParams {

@@ -59,7 +59,7 @@ __device__ __forceinline__ float row_reduce(float v, float* smem, int row_in_cta
 template <typename T, int kTPR, int kChunks, int kThreads, int kR, int kStep>
 __global__ void __launch_bounds__(kThreads) kda_rms_norm_kernel(const NormParams p) {
   using Raw = typename T::Raw;
-  static_assert(kThreads % kTPR == 0 && kTPR % 16 == 0, "whole rows and scale groups");
+  static_assert(kThreads % kTPR == 0, "whole rows");
   static_assert(kR == 1 || kTPR <= 32, "one row per thread where warps share it");
   __shared__ float s_sum[kThreads / 32], s_max[kThreads / 32];
   constexpr int kRows = kThreads / kTPR;     // rows side by side; the CTA has kR times as many
@@ -231,7 +231,7 @@ __global__ void __launch_bounds__(kThreads) kda_rms_norm_kernel(const NormParams
       if (n[r] > 0 && j == 0) p.scales[row] = amax * (1.f / kE4m3Max);
 #pragma unroll
       for (int i = 0; i < kChunks; ++i) factor[i] = kE4m3Max * rcp_approx(amax);
-    } else {
+    } else if constexpr (kTPR % 16 == 0) {     // (shorter rows are one group)
 #pragma unroll
       for (int i = 0; i < kChunks; ++i) {
         float m = amax_of(r, i);
@@ -280,9 +280,11 @@ bool go(const NormParams& p, cudaStream_t s) {
 }
 
 template <typename T>
-bool launch(const NormParams& p, cudaStream_t s) {
+bool launch(NormParams p, cudaStream_t s) {
   // The fewest threads whose registers hold the row in few chunks each.
   const int W = p.width;
+  if (W <= 128) p.group = 0;      // one scale group: the row
+  if (W <= 64) return go<T, 8, 1, 128, 4>(p, s);
   if (W <= 128) return go<T, 16, 1, 128, 4>(p, s);
   if (W <= 256) return go<T, 32, 1, 128, 2>(p, s);
   if (W <= 512) return go<T, 32, 2, 128>(p, s);

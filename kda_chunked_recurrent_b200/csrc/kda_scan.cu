@@ -26,6 +26,7 @@
 //
 // Tokens.  Four state elements (16 bytes) per thread, the state read and written once; a
 // CTA takes four sequences so that A is read once for them.
+#include <algorithm>
 #include <type_traits>
 
 #include "kda_layer.cuh"
@@ -283,8 +284,9 @@ __global__ void __launch_bounds__(kThreads, 2) kda_scan_prefill_kernel(const Sca
   const int seg = blockIdx.x % kSplit, unit = blockIdx.x / kSplit;
   int32_t n = unit / tiles;
   const int tile = unit - n * tiles;
-  // Ragged batches: the longest sequences first, so that the last CTAs to start are short.
-  if (p.seq.cu != nullptr && p.seq.num > 1 && p.seq.num <= kThreads) {
+  // Ragged batches that do not run all at once: the longest sequences first, so that the last
+  // CTAs to start are short (16 prompts of 1 to 4096 rows: 554 -> 419 us).
+  if (p.longest_first) {
     int32_t* lens = reinterpret_cast<int32_t*>(smem_raw);
     int32_t* found = lens + kThreads;
     int32_t mine = 0;
@@ -451,8 +453,14 @@ __global__ void __launch_bounds__(kThreads, 2) kda_scan_prefill_kernel(const Sca
           bring(row, r.dt[o][ht], DT + o * p.ds, p.dt, n_row[o]);
           if (gated) bring(row, r.z[o][ht], Z + o * p.zs, p.z, n_row[o]);
         }
-        bring(bc, r.b[ht], Bp, p.B, n_bc);
-        bring(bc, r.c[ht], Cp, p.Cm, n_bc);
+        if (p.vec_bc) {
+          constexpr int kBc = kQ * C::kElem;
+          copy_async<kBc>(smem_u32(r.b[ht]), n_bc > 0 ? Bp : p.B, n_bc <= 0);
+          copy_async<kBc>(smem_u32(r.c[ht]), n_bc > 0 ? Cp : p.Cm, n_bc <= 0);
+        } else {
+          bring(bc, r.b[ht], Bp, p.B, n_bc);
+          bring(bc, r.c[ht], Cp, p.Cm, n_bc);
+        }
       } else {
         Vec<T, kE> vx[2], vd[2], vz[2];
         Vec<T, kQ> vb, vc;
@@ -462,8 +470,13 @@ __global__ void __launch_bounds__(kThreads, 2) kda_scan_prefill_kernel(const Sca
           vd[o].template load<false>(DT + o * p.ds, n_row[o]);
           if (gated) vz[o].template load<false>(Z + o * p.zs, n_row[o]);
         }
-        vb.template load<false>(Bp, n_bc);
-        vc.template load<false>(Cp, n_bc);
+        if (p.vec_bc && n_bc > 0) {
+          vb.template load<true>(Bp);
+          vc.template load<true>(Cp);
+        } else {
+          vb.template load<false>(Bp, n_bc);
+          vc.template load<false>(Cp, n_bc);
+        }
 #pragma unroll
         for (int o = 0; o < 2; ++o) {
           vx[o].template store<true>(r.x[o][ht]);
@@ -603,55 +616,91 @@ __global__ void __launch_bounds__(kThreads, 2) kda_scan_prefill_kernel(const Sca
 // A lane's first duty is one of the four sequences: it alone loads dt, x and z there and takes
 // the softplus and the gate, and hands them to the other lanes of the channel; and it is left
 // with the sum of that sequence after the exchange.
-// kOne: one new token each and no step states.
-template <typename T, int kL, bool kVec, bool kOne>
-__global__ void __launch_bounds__(256, (kOne ? 3 : 1) + (sizeof(typename T::Raw) == 2))
-kda_scan_decode_kernel(const ScanParams p) {
+enum Tokens {
+  kOne,      // one new token each, no step states
+  kFew,      // some each, small batches: the next token's rows are loaded a token ahead
+  kMany,     // some each, large batches: more warps instead (ahead, the registers of FP32 rows
+             // left an SM eight warps: 718 sequences of 7 tokens of 736 channels 135 us)
+  kPrompts,  // packed sequences of few rows each
+};
+template <typename T, int kL, bool kVec, Tokens kMode>
+__global__ void __launch_bounds__(256, kMode == kOne    ? (sizeof(typename T::Raw) == 2 ? 4 : 3)
+                                       : kMode == kMany ? (sizeof(typename T::Raw) == 2 ? 3 : 2)
+                                       : sizeof(typename T::Raw) == 2 ? 2 : 1)
+kda_scan_token_kernel(const ScanParams p) {
   using Raw = typename T::Raw;
   constexpr int kCh = 256 / kL;     // channels per CTA
-  constexpr int kN = 4;             // sequences per CTA
+  constexpr int kN = 4;             // sequences at a time
   const int q = threadIdx.x % kL, cl = threadIdx.x / kL, own = q & 3;
-  const int tiles = p.tiles_per_group;                 // channel tiles (groups may share one)
-  const int tile = blockIdx.x % tiles;
-  const int ch = tile * kCh + cl;
-  const bool on = ch < p.channels;
-  const int c = on ? ch : p.channels - 1;              // idle threads follow the last channel
-  const int e0 = 4 * q, count = on ? p.size - e0 : 0;  // state elements of this thread
-  const int32_t T_new = kOne ? 1 : p.seq.fixed_len;
-  const int64_t state_at = static_cast<int64_t>(c) * p.size + e0;
+  const int e0 = 4 * q;                                // first state element of this thread
+  const int32_t T_each = kMode == kOne ? 1 : p.seq.fixed_len;   // (not of prompts)
   const int64_t state_slot_size = static_cast<int64_t>(p.channels) * p.size;
-  const int64_t bc_at = static_cast<int64_t>(c / p.per_group) * p.size + e0;
-  const int64_t b_seq = T_new * p.bs, c_seq = T_new * p.cs;   // from a sequence to the next
+  // A unit is a tile of channels of kN sequences; a CTA takes a run of units, whose tiles rarely
+  // change (what belongs to the channels is then read again).
+  const int32_t batches = (p.seq.num + kN - 1) / kN;
+  const int64_t units = static_cast<int64_t>(batches) * p.tiles_per_group;
+  const int64_t unit_end = units * (blockIdx.x + 1) / gridDim.x;
+  int32_t tile = -1, c = 0, count = 0;
+  bool on = false;
+  int64_t state_at = 0, bc_at = 0;
   float2 A[2];
-  {
-    Vec<F32, 4> av;
-    if (count > 0) av.template load<kVec>(p.A_log + state_at, count);
-    else av.clear();
-    float a[4];
-    av.unpack(a);
-#pragma unroll
-    for (int i = 0; i < 4; ++i) a[i] = i < count ? -kLog2e * ex2_full(a[i]) : 0.f;
-    A[0] = make_float2(a[0], a[1]);
-    A[1] = make_float2(a[2], a[3]);
-  }
-  const float bias = p.dt_bias != nullptr ? p.dt_bias[c] : 0.f;
-  const float skip = p.D != nullptr ? p.D[c] : 0.f;
-  const int32_t first = static_cast<int32_t>(blockIdx.x / tiles) * p.seqs_per_cta;
-  const int32_t last = min(first + p.seqs_per_cta, p.seq.num);
+  float bias = 0.f, skip = 0.f;
 
-  for (int32_t n0 = first; n0 < last; n0 += kN) {
+  for (int64_t unit = units * blockIdx.x / gridDim.x; unit < unit_end; ++unit) {
+    const int32_t t_of = static_cast<int32_t>(unit / batches);
+    const int32_t n0 = static_cast<int32_t>(unit - static_cast<int64_t>(t_of) * batches) * kN;
+    if (t_of != tile) {
+      tile = t_of;
+      const int ch = tile * kCh + cl;
+      on = ch < p.channels;
+      c = on ? ch : p.channels - 1;                    // idle threads follow the last channel
+      count = on ? p.size - e0 : 0;                    // state elements of this thread
+      state_at = static_cast<int64_t>(c) * p.size + e0;
+      bc_at = static_cast<int64_t>(c / p.per_group) * p.size + e0;
+      Vec<F32, 4> av;
+      if (count > 0) av.template load<kVec>(p.A_log + state_at, count);
+      else av.clear();
+      float a[4];
+      av.unpack(a);
+#pragma unroll
+      for (int i = 0; i < 4; ++i) a[i] = i < count ? -kLog2e * ex2_full(a[i]) : 0.f;
+      A[0] = make_float2(a[0], a[1]);
+      A[1] = make_float2(a[2], a[3]);
+      bias = p.dt_bias != nullptr ? p.dt_bias[c] : 0.f;
+      skip = p.D != nullptr ? p.D[c] : 0.f;
+    }
     int32_t slot[kN];
 #pragma unroll
     for (int s = 0; s < kN; ++s)
-      slot[s] = n0 + s < p.seq.num ? state_slot(p.slot, n0 + s, p.pool, p.status,
-                                                tile == 0 && threadIdx.x == 0)
-                                   : -1;
+      slot[s] = n0 + s < p.seq.num && p.state != nullptr
+                    ? state_slot(p.slot, n0 + s, p.pool, p.status, tile == 0 && threadIdx.x == 0)
+                    : -1;
+    // first rows and numbers of rows
+    int32_t row[kN], rows[kN], T_new = T_each;
+    if constexpr (kMode == kPrompts) T_new = 0;
+#pragma unroll
+    for (int s = 0; s < kN; ++s) {
+      if constexpr (kMode == kPrompts) {
+        row[s] = rows[s] = 0;
+        if (n0 + s < p.seq.num) {
+          int32_t end;
+          p.seq.range(n0 + s, row[s], end);
+          rows[s] = end - row[s];
+        }
+        T_new = max(T_new, rows[s]);
+      } else {
+        row[s] = (n0 + s) * T_each;
+        rows[s] = slot[s] >= 0 ? T_each : 0;
+      }
+    }
     float2 h[kN][2];
     const auto state_of = [&](int s) { return p.state + slot[s] * state_slot_size + state_at; };
 #pragma unroll
     for (int s = 0; s < kN; ++s) {
       Vec<F32, 4> v;
-      if (slot[s] >= 0 && count > 0) v.template load<kVec>(state_of(s), count);
+      bool old = slot[s] >= 0;
+      if constexpr (kMode == kPrompts) old = old && (p.has == nullptr || p.has[n0 + s] != 0);
+      if (old && count > 0) v.template load<kVec>(state_of(s), count);
       else v.clear();
       h[s][0] = make_float2(__uint_as_float(v.w[0]), __uint_as_float(v.w[1]));
       h[s][1] = make_float2(__uint_as_float(v.w[2]), __uint_as_float(v.w[3]));
@@ -664,27 +713,27 @@ kda_scan_decode_kernel(const ScanParams p) {
       v.w[3] = __float_as_uint(h[s][1].y);
       v.template store<kVec>(to, count);
     };
-    // rows of token 0; token t is t strides on
-    const int64_t r_own = static_cast<int64_t>(n0 + own) * T_new;
-    const int64_t r_first = static_cast<int64_t>(n0) * T_new;
-    const bool own_in = n0 + own < p.seq.num;
-    const bool own_live = own_in && (own == 0   ? slot[0]
-                                     : own == 1 ? slot[1]
-                                     : own == 2 ? slot[2]
-                                                : slot[3]) >= 0;
+    // the lane's own sequence: rows of token 0; token t is t strides on
+    const auto mine = [&](const int32_t (&v)[kN]) {
+      return own == 0 ? v[0] : own == 1 ? v[1] : own == 2 ? v[2] : v[3];
+    };
+    const int32_t rows_own = mine(rows);
+    const int64_t r_own = mine(row);
     const Raw* X = static_cast<const Raw*>(p.x) + r_own * p.xs + c;
     const Raw* DT = static_cast<const Raw*>(p.dt) + r_own * p.ds + c;
     const Raw* Z = static_cast<const Raw*>(p.z) + r_own * p.zs + c;
     Raw* out = static_cast<Raw*>(p.out) + r_own * p.channels + c;
-    const Raw* Bp = static_cast<const Raw*>(p.B) + r_first * p.bs + bc_at;
-    const Raw* Cp = static_cast<const Raw*>(p.Cm) + r_first * p.cs + bc_at;
+    // B and C of the first sequence (prompts: each sequence's rows are found on their own)
+    const int64_t b_seq = T_each * p.bs, c_seq = T_each * p.cs;
+    const Raw* Bp = static_cast<const Raw*>(p.B) + static_cast<int64_t>(row[0]) * p.bs + bc_at;
+    const Raw* Cp = static_cast<const Raw*>(p.Cm) + static_cast<int64_t>(row[0]) * p.cs + bc_at;
     struct Row {
       Raw x, dt, z;
       Vec<T, 4> b[kN], c[kN];
     };
-    const auto fetch = [&](Row& r) {       // the rows of the next token
+    const auto fetch = [&](Row& r, int32_t t) {       // token t's rows; the pointers move on
       r.x = r.dt = r.z = Raw(0);
-      if (own_live) {
+      if (t < rows_own) {
         r.x = *X;
         r.dt = *DT;
         if (p.z != nullptr) r.z = *Z;
@@ -692,7 +741,11 @@ kda_scan_decode_kernel(const ScanParams p) {
       const Raw *bs = Bp, *cs = Cp;
 #pragma unroll
       for (int s = 0; s < kN; ++s) {
-        if (slot[s] >= 0 && count > 0) {
+        if constexpr (kMode == kPrompts) {
+          bs = static_cast<const Raw*>(p.B) + static_cast<int64_t>(row[s] + t) * p.bs + bc_at;
+          cs = static_cast<const Raw*>(p.Cm) + static_cast<int64_t>(row[s] + t) * p.cs + bc_at;
+        }
+        if (t < rows[s] && count > 0) {
           r.b[s].template load<kVec>(bs, count);
           r.c[s].template load<kVec>(cs, count);
         } else {
@@ -702,7 +755,7 @@ kda_scan_decode_kernel(const ScanParams p) {
         bs += b_seq;
         cs += c_seq;
       }
-      if constexpr (!kOne) {
+      if constexpr (kMode != kOne) {
         X += p.xs;
         DT += p.ds;
         Z += p.zs;
@@ -710,13 +763,16 @@ kda_scan_decode_kernel(const ScanParams p) {
         Cp += p.cs;
       }
     };
+    constexpr bool kAhead = kMode == kFew || kMode == kPrompts;
     Row cur, next;
-    fetch(cur);
+    if (kMode != kMany) fetch(cur, 0);
     for (int32_t t = 0; t < T_new; ++t) {
-      if (!kOne && t + 1 < T_new) fetch(next);
+      if (kMode == kMany) fetch(cur, t);
+      if (kAhead && t + 1 < T_new) fetch(next, t + 1);
       const float x = T::to(cur.x);
       float d = T::to(cur.dt) + bias;
       if (p.softplus) d = softplus(d);
+      if (kMode == kPrompts && t >= rows_own) d = 0.f;     // behind the end: the state stays
       const float dx = d * x;
       float part[kN];
 #pragma unroll
@@ -752,16 +808,18 @@ kda_scan_decode_kernel(const ScanParams p) {
         const float z = T::to(cur.z);
         y *= z * sigmoid(z);
       }
-      // a padding row's output is zero
-      if (on && q < 4 && own_in) *out = T::from(own_live ? y : 0.f);
-      if constexpr (!kOne) {
+      // a padding row's output is zero; a prompt has no rows behind its end
+      const bool live = t < rows_own;
+      if (on && q < 4 && (kMode == kPrompts ? live : n0 + own < p.seq.num))
+        *out = T::from(live ? y : 0.f);
+      if constexpr (kMode != kOne) {
         out += p.channels;
-        cur = next;
-        if (p.steps != nullptr && count > 0) {
+        if (kAhead) cur = next;
+        if (kMode != kPrompts && p.steps != nullptr && count > 0) {
 #pragma unroll
           for (int s = 0; s < kN; ++s)
             if (slot[s] >= 0)
-              put_state(s, p.steps + ((r_first + s * T_new + t) * state_slot_size + state_at));
+              put_state(s, p.steps + (static_cast<int64_t>(row[s] + t) * state_slot_size + state_at));
         }
       }
     }
@@ -781,16 +839,17 @@ bool whole(const void* q, int64_t stride_bytes, int bytes) {
 }
 
 template <typename T, typename C, int kSplit>
-bool go_prefill(ScanParams p, cudaStream_t s) {
+bool go_prefill(ScanParams p, int sms, cudaStream_t s) {
   p.tiles_per_group = (p.per_group + C::kCH - 1) / C::kCH;
   constexpr int e = sizeof(typename T::Raw), kRow = C::kE * e, kBc = C::kQ * e;
+  p.vec_bc = whole(p.B, p.bs * e, kBc) && whole(p.Cm, p.cs * e, kBc) && p.size % C::kQ == 0;
   const bool vec = whole(p.x, p.xs * e, kRow) && whole(p.dt, p.ds * e, kRow) &&
                    whole(p.z, p.zs * e, kRow) &&
                    whole(p.out, static_cast<int64_t>(p.channels) * e, kRow) &&
-                   p.per_group % C::kE == 0 && whole(p.B, p.bs * e, kBc) &&
-                   whole(p.Cm, p.cs * e, kBc) && p.size % C::kQ == 0;
+                   p.per_group % C::kE == 0 && p.vec_bc;
   const int64_t grid = static_cast<int64_t>(p.seq.num) * p.groups * p.tiles_per_group * kSplit;
   if (grid > INT32_MAX) return false;
+  p.longest_first = p.seq.cu != nullptr && p.seq.num > 1 && p.seq.num <= kThreads && grid > sms;
   constexpr int kSmem = sizeof(typename C::Smem) + (kSplit > 1 ? sizeof(Exchange<C>) : 0);
   static_assert(kSmem <= 227 * 1024, "shared memory of a CTA");
   const auto kernel = vec ? kda_scan_prefill_kernel<T, C, true, kSplit>
@@ -825,14 +884,54 @@ bool pick_prefill(const ScanParams& p, int64_t max_rows, int sms, cudaStream_t s
   const int64_t tiles = static_cast<int64_t>(p.seq.num) * p.groups *
                         ((p.per_group + C::kCH - 1) / C::kCH);
   if (max_rows >= 512) {
-    if (tiles * 32 <= 7LL * sms) return go_prefill<T, C, 8>(p, s);
-    if (tiles * 4 <= 2LL * sms) return go_prefill<T, C, 4>(p, s);
+    if (tiles * 32 <= 7LL * sms) return go_prefill<T, C, 8>(p, sms, s);
+    if (tiles * 4 <= 2LL * sms) return go_prefill<T, C, 4>(p, sms, s);
   }
-  return go_prefill<T, C, 1>(p, s);
+  return go_prefill<T, C, 1>(p, sms, s);
+}
+
+template <typename T, int kL>
+bool go_tokens(ScanParams p, bool prompts, int sms, cudaStream_t s) {
+  constexpr int kCh = 256 / kL, kN = 4, e = sizeof(typename T::Raw);
+  p.tiles_per_group = (p.channels + kCh - 1) / kCh;
+  const bool vec = p.size % 4 == 0 && whole(p.B, p.bs * e, 4 * e) && whole(p.Cm, p.cs * e, 4 * e) &&
+                   whole(p.A_log, 0, 16);
+  const bool one = !prompts && p.seq.fixed_len == 1 && p.steps == nullptr;
+  const int64_t units =
+      static_cast<int64_t>((p.seq.num + kN - 1) / kN) * p.tiles_per_group;
+  if (units > INT32_MAX) return false;
+  // One token each is short work: as many CTAs as the SMs hold share the units evenly.
+  const int64_t grid = one ? std::min<int64_t>(units, sms * (e == 2 ? 4LL : 3LL)) : units;
+  const auto go = [&](auto vec_kernel, auto any_kernel) {
+    (vec ? vec_kernel : any_kernel)<<<static_cast<unsigned>(grid), 256, 0, s>>>(p);
+    return true;
+  };
+  if (prompts)
+    return go(kda_scan_token_kernel<T, kL, true, kPrompts>,
+              kda_scan_token_kernel<T, kL, false, kPrompts>);
+  if (one)
+    return go(kda_scan_token_kernel<T, kL, true, kOne>, kda_scan_token_kernel<T, kL, false, kOne>);
+  if (units > 2LL * sms)
+    return go(kda_scan_token_kernel<T, kL, true, kMany>,
+              kda_scan_token_kernel<T, kL, false, kMany>);
+  return go(kda_scan_token_kernel<T, kL, true, kFew>, kda_scan_token_kernel<T, kL, false, kFew>);
+}
+
+template <typename T>
+bool launch_tokens(const ScanParams& p, bool prompts, int sms, cudaStream_t s) {
+  if (p.size > 64) return go_tokens<T, 32>(p, prompts, sms, s);
+  if (p.size > 32) return go_tokens<T, 16>(p, prompts, sms, s);
+  if (p.size > 16) return go_tokens<T, 8>(p, prompts, sms, s);
+  return go_tokens<T, 4>(p, prompts, sms, s);
 }
 
 template <typename T>
 bool launch_prefill(const ScanParams& p, int64_t max_rows, int sms, cudaStream_t s) {
+  // Many sequences of few rows: row by row in the token kernel.  A block of the kernel above
+  // costs a CTA about 5 us however few rows it has.  32 sequences of 1 / 4 / 16 / 32 rows of
+  // 2048 channels, us, token kernel and this: 6.3 / 10.2 / 20.6 / 37 and 22.7 / 22.7 / 27 / 33.
+  const int64_t ctas = static_cast<int64_t>(p.seq.num) * p.channels / 32;
+  if (max_rows <= 16 && ctas > 2LL * sms) return launch_tokens<T>(p, true, sms, s);
   if (p.size > 64) return pick_prefill<T, Cfg<T, 128, 8>>(p, max_rows, sms, s);
   if (p.size > 32) return pick_prefill<T, Cfg<T, 64, 8>>(p, max_rows, sms, s);
   if (p.size > 16) return pick_prefill<T, Cfg<T, 32, 4>>(p, max_rows, sms, s);
@@ -841,35 +940,7 @@ bool launch_prefill(const ScanParams& p, int64_t max_rows, int sms, cudaStream_t
   // 159 / 159.
   if (static_cast<int64_t>(p.seq.num) * p.channels <= 16LL * sms)
     return pick_prefill<T, Cfg<T, 16, 2>>(p, max_rows, sms, s);
-  return go_prefill<T, Cfg<T, 16, 4>, 1>(p, s);
-}
-
-template <typename T, int kL>
-bool go_decode(ScanParams p, int sms, cudaStream_t s) {
-  constexpr int kCh = 256 / kL, kN = 4, e = sizeof(typename T::Raw);
-  p.tiles_per_group = (p.channels + kCh - 1) / kCh;
-  const bool vec = p.size % 4 == 0 && whole(p.B, p.bs * e, 4 * e) && whole(p.Cm, p.cs * e, 4 * e) &&
-                   whole(p.A_log, 0, 16);
-  // More sequences per CTA share its A once the batch fills the SMs many times without that.
-  p.seqs_per_cta = static_cast<int64_t>(p.seq.num) * p.tiles_per_group >= 64LL * sms ? 2 * kN : kN;
-  const int64_t grid = static_cast<int64_t>((p.seq.num + p.seqs_per_cta - 1) / p.seqs_per_cta) *
-                       p.tiles_per_group;
-  if (grid > INT32_MAX) return false;
-  const bool one = p.seq.fixed_len == 1 && p.steps == nullptr;
-  const auto kernel = vec ? (one ? kda_scan_decode_kernel<T, kL, true, true>
-                                 : kda_scan_decode_kernel<T, kL, true, false>)
-                          : (one ? kda_scan_decode_kernel<T, kL, false, true>
-                                 : kda_scan_decode_kernel<T, kL, false, false>);
-  kernel<<<static_cast<unsigned>(grid), 256, 0, s>>>(p);
-  return true;
-}
-
-template <typename T>
-bool launch_decode(const ScanParams& p, int sms, cudaStream_t s) {
-  if (p.size > 64) return go_decode<T, 32>(p, sms, s);
-  if (p.size > 32) return go_decode<T, 16>(p, sms, s);
-  if (p.size > 16) return go_decode<T, 8>(p, sms, s);
-  return go_decode<T, 4>(p, sms, s);
+  return go_prefill<T, Cfg<T, 16, 4>, 1>(p, sms, s);
 }
 
 }  // namespace scan
@@ -881,9 +952,9 @@ bool launch_scan_prefill(const ScanParams& p, int64_t max_rows, int dtype, int s
   return scan::launch_prefill<F32>(p, max_rows, sms, s);
 }
 bool launch_scan_decode(const ScanParams& p, int dtype, int sms, cudaStream_t s) {
-  if (dtype == 0) return scan::launch_decode<Bf16>(p, sms, s);
-  if (dtype == 1) return scan::launch_decode<F16>(p, sms, s);
-  return scan::launch_decode<F32>(p, sms, s);
+  if (dtype == 0) return scan::launch_tokens<Bf16>(p, false, sms, s);
+  if (dtype == 1) return scan::launch_tokens<F16>(p, false, sms, s);
+  return scan::launch_tokens<F32>(p, false, sms, s);
 }
 
 }  // namespace layer

@@ -248,3 +248,14 @@ def test_prompts_few_channels_small_steps():
     y, yb, hs, es = scan(f64(x), f64(dt), f64(A_log), f64(B), f64(C), f64(Dv), f64(z), None, h0, False)
     close(out, y, yb, torch.float32, "rows")
     close(pool[0], hs[-1], es[-1], torch.float32, "state")
+
+
+# many sequences of few rows each
+@pytest.mark.parametrize("dtype,D,S,G,N", [("bf16", 1024, 16, 1, 20), ("f32", 1030, 13, 2, 20),
+                                           ("f16", 1024, 128, 4, 12), ("bf16", 2051, 20, 1, 7)])
+def test_prompts_many_of_few_rows(dtype, D, S, G, N):
+    r = np.random.RandomState(4)
+    lens = [int(v) for v in r.randint(0, 6, N - 1)] + [16]
+    _check_prefill(lens, D, S, G, dtype, sliced=dtype == "f32")
+    _check_prefill([1] * N, D, S, G, dtype, state=False, gate=False)
+    _check_prefill([3] * N, D, S, G, dtype, fixed=True, hint=False)
