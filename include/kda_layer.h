@@ -20,8 +20,12 @@
  * nearest even.
  *
  * Strides count elements.  Rows may lie apart (a slice of a fused projection); the
- * elements of a row are adjacent.  Any stride and any element-aligned address is accepted;
- * 16-byte aligned rows whose length is a multiple of 16 bytes are the fast case.
+ * elements of a row are adjacent.  Any stride and any element-aligned address is accepted
+ * (scan states and their step_states lie on 16 bytes); 16-byte aligned rows whose length is
+ * a multiple of 16 bytes are the fast case.
+ *
+ * Not finite values: an infinity or a NaN stays in the windows, the channel's states or the
+ * row that it is in; the SiLU of minus infinity is a NaN.
  */
 #ifndef KDA_LAYER_H_
 #define KDA_LAYER_H_
@@ -124,7 +128,8 @@ typedef struct {
   int32_t pool_size;   /* slots in `state` (>= 1 where there is one)                     */
   int32_t dtype;       /* kda_dtype_t of x, dt, B, C, z and out                          */
   int32_t max_seqlen;  /* prompts: an upper bound on every length; 0 = not known.  A hint
-                          for the launch shape: results do not depend on it              */
+                          for the launch shape (the order of FP32 sums may depend on it);
+                          decode: not read                                               */
   int64_t x_stride, dt_stride, z_stride; /* elements between rows, >= channels           */
   int64_t b_stride, c_stride;            /* elements between rows of B and C; the
                                             [groups, state_size] of a row are contiguous */

