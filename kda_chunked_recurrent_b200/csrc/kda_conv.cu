@@ -6,12 +6,12 @@
 // Every channel is on its own and every input row is needed by W outputs, so the work is a
 // copy with a little arithmetic: 2 bytes in, 2 bytes out, W FMAs and (SiLU) two special
 // functions per element.  Bound: HBM, with the special functions not far behind (29K rows of
-// 4608 BF16 channels: 81 us of bytes, 58 us of special functions; 105 to 110 us measured, 4.9
+// 4608 BF16 channels: 81 us of bytes, 58 us of special functions; 97 us measured, 5.5
 // TB/s).
 //
 // Prompts.  A thread owns kV adjacent channels and walks strips of kStrip rows: all rows
-// of a strip are loaded at once (the loads of a strip are what keeps HBM busy), the W - 1
-// rows before it are carried over from the strip before or re-read once per CTA.  The
+// of a strip are loaded at once, a strip ahead (these loads are what keeps HBM busy), the
+// W - 1 rows before it are carried over from the strip before or re-read once per CTA.  The
 // first W - 1 rows of every sequence need its state instead; they, and the state that the
 // sequence leaves, belong to a second set of CTAs, one per (sequence, column block).  Since
 // one thread there reads the old state rows of its channels and then writes the new ones,
@@ -19,7 +19,7 @@
 //
 // Tokens.  One thread per kV channels of a sequence: state rows and new rows in, outputs
 // and the shifted state out (1024 sequences of 4608 BF16 channels 16.5 us, 4.6 TB/s).
-#include <type_traits>
+#include <algorithm>
 
 #include "kda_layer.cuh"
 
@@ -27,7 +27,7 @@ namespace kda {
 namespace layer {
 namespace conv {
 
-constexpr int kStrip = 8;
+constexpr int kStrip = 6;
 
 // kVec: every row, the weights and the outputs may be read and written 16 bytes at a time
 // (then a thread's channels lie in one part); else element by element.
@@ -130,27 +130,40 @@ __device__ __forceinline__ void strips_body(const ConvParams& p, int group, int 
   const int64_t xs = p.x_stride;
   // row t0 - (W - 1) + i is row i of px; it is only looked at where it exists
   const Raw* px = static_cast<const Raw*>(p.x) + (static_cast<int64_t>(t0) - (W - 1)) * xs + c0;
-  Vec<T, kV> r[W - 1 + kStrip];
-  const auto fetch = [&](auto from) {
-    if (on && t0 >= W - 1 && t0 + kStrip <= rows) {
+  Vec<T, kV> r[W - 1 + kStrip], next[kStrip];
+  // the rows of the strip behind, while this one is worked on
+  const auto ahead = [&] {
+    const Raw* q = px + (W - 1 + kStrip) * xs;
+    if (on && t0 + 2 * kStrip <= rows) {
 #pragma unroll
-      for (int i = decltype(from)::value; i < W - 1 + kStrip; ++i) r[i].template load<kVec>(px + i * xs);
+      for (int i = 0; i < kStrip; ++i) next[i].template load<kVec>(q + i * xs);
     } else {
 #pragma unroll
-      for (int i = decltype(from)::value; i < W - 1 + kStrip; ++i) {
-        const int32_t t = t0 - (W - 1) + i;
-        if (on && t >= 0 && t < rows) r[i].template load<kVec>(px + i * xs);
-        else r[i].clear();
+      for (int i = 0; i < kStrip; ++i) {
+        if (on && t0 + kStrip + i < rows) next[i].template load<kVec>(q + i * xs);
+        else next[i].clear();
       }
     }
   };
-  fetch(std::integral_constant<int, 0>());
+  if (on && t0 >= W - 1 && t0 + kStrip <= rows) {
+#pragma unroll
+    for (int i = 0; i < W - 1 + kStrip; ++i) r[i].template load<kVec>(px + i * xs);
+  } else {
+#pragma unroll
+    for (int i = 0; i < W - 1 + kStrip; ++i) {
+      const int32_t t = t0 - (W - 1) + i;
+      if (on && t >= 0 && t < rows) r[i].template load<kVec>(px + i * xs);
+      else r[i].clear();
+    }
+  }
   Taps<W, kVec> taps;
   if (on) taps.load(p, c0);
   const Out<T, kVec> out(p, on ? c0 : 0);
   int32_t n = find_seq(p.seq, t0), a, b;
   p.seq.range(n, a, b);
   while (true) {
+    const bool more = t0 + kStrip < t_end;
+    if (more) ahead();
     float u[W][kV];
 #pragma unroll
     for (int j = 0; j < W - 1; ++j) r[j].unpack(u[j]);
@@ -179,12 +192,13 @@ __device__ __forceinline__ void strips_body(const ConvParams& p, int group, int 
         row(i, on && t >= a + (W - 1) && t < b);
       }
     }
-    if (t0 + kStrip >= t_end) break;
+    if (!more) break;
 #pragma unroll
     for (int j = 0; j < W - 1; ++j) r[j] = r[kStrip + j];
+#pragma unroll
+    for (int i = 0; i < kStrip; ++i) r[W - 1 + i] = next[i];
     t0 += kStrip;
     px += kStrip * xs;
-    fetch(std::integral_constant<int, W - 1>());
   }
 }
 
@@ -351,11 +365,12 @@ template <typename T>
 bool launch_prefill(ConvParams p, int W, int sms, cudaStream_t s) {
   const Shape sh = columns(p.C, p.vec ? Cfg<true>::kV : Cfg<false>::kV);
   p.strips = (p.seq.rows + kStrip - 1) / kStrip;
-  // Adjacent strips share the weights and the W - 1 rows between them; a CTA walks
-  // four while that still leaves every SM many CTAs (one, two, four of 29K rows of 4608
-  // channels: 117.6, 109.1, 105.3 us).
-  p.strips_per_cta =
-      static_cast<int64_t>(p.strips) * sh.cols >= 32LL * sms ? 4 : 1;
+  // Adjacent strips share the weights and the W - 1 rows between them, and the next one's rows
+  // are on their way while one is worked on; a CTA walks up to eight while every SM still gets
+  // eight CTAs (29K rows of 4608 channels, us: strips of 4 / 6 / 8 rows, eight each, 105 / 96.6 /
+  // 100.5; without the next strip's rows, 8 rows, four each, 107.4).
+  p.strips_per_cta = static_cast<int32_t>(std::max<int64_t>(
+      1, std::min<int64_t>(8, static_cast<int64_t>(p.strips) * sh.cols / (8LL * sms))));
   const int64_t groups = (p.strips + p.strips_per_cta - 1) / p.strips_per_cta;
   const int64_t grid = (groups + p.seq.num) * sh.cols;
   if (grid > INT32_MAX) return false;
