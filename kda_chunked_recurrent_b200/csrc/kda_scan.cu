@@ -19,14 +19,15 @@
 // and d x once per (row, channel) one block ahead, and, one block behind, add the lanes' parts
 // of the sums and write the output rows (skip, gate, rounding).  One barrier a block.
 //
-// Measured: 8192 rows of 4096 BF16 channels 293 us, of which the exponentials alone would
+// Measured: 8192 rows of 4096 BF16 channels 285 us, of which the exponentials alone would
 // take 150 at their rate, all special functions 171 (128 of 148 SMs have work); 16 ragged
-// prompts of 2048 FP16 channels 373 us, against 260.  With one scan and one helper warp on a
-// scheduler the rest is latency: a row takes 69 clocks, 45 in the scan warp when it runs alone
-// (33 for its 4 exponentials a lane), 24 more with the helpers' work.  Tried and dropped, us
+// prompts of 2048 FP16 channels 365 us, against 260.  With one scan and one helper warp on a
+// scheduler the rest is latency: a row takes 67 clocks, of which the scan warp's 4
+// exponentials a lane are 33 and the helpers' work on the same units 20.  Tried and dropped, us
 // for the first: one exponential in eight on the FMA pipe 337 (of 312 then), B and C in FP32
-// and d in pairs in shared memory 329 (of 293), separate warps for staging and writing 283,
-// but 386 of 373 for the ragged prompts, two channels per lane 419 (of 401, ragged).
+// and d in pairs in shared memory 306 (of 285; in pairs alone 294), separate warps for staging
+// and writing 283 (of 293), but 386 of 373 for the ragged prompts, two channels per lane 419
+// (of 401, ragged).
 //
 // Tokens.  Four state elements (16 bytes) per thread, the state read and written once; four
 // sequences at a time.  256 sequences of 4096 channels 32.9 us, 4.3 TB/s.
@@ -346,7 +347,10 @@ __global__ void __launch_bounds__(kThreads, 2) kda_scan_prefill_kernel(const Sca
 
   if (warp < kSW) {
     // ---- scan warps
-    const int q = lane % C::kL, ch0 = warp * C::kCW + lane / C::kL;   // place
+    // Adjacent lanes take adjacent channels of one place of the state: a read of B or C is
+    // then one address for 8 lanes side by side, one pass of shared memory and not the two that
+    // addresses alternating from lane to lane take (293 -> 285 us; state size 64 258 -> 215).
+    const int q = lane / C::kCW, ch0 = warp * C::kCW + lane % C::kCW;   // place
     const int ch = C::channel(ch0);
     float2 h[Ops<C>::kP];
     float A[C::kS];
@@ -890,9 +894,9 @@ bool go_prefill(ScanParams p, int sms, cudaStream_t s) {
 // Few channels and many rows: the rows are shared by a cluster of 8 or 4 CTAs.  A run is taken
 // twice, so the time falls to a quarter or a half at best.  One sequence, 16-bit rows, us, by
 // one CTA / 4 / 8 (256 channels; 592; 1024):
-//    512 rows   18.2 / 12.5 / 12.5;   18.7 / 16.6 / 20.0
-//   2048 rows   57.6 / 31.0 / 26.9;   59.7 / 45.3 / 46.0
-//   4096 rows    110 / 55.6 / 45.3;                         119 / 88 / 94
+//    512 rows   16.5 / 12.4 / 12.3;   16.5 / 16.0 / 18.9
+//   2048 rows   52.6 / 30.9 / 24.8;   55.4 / 43.2 / 44.2
+//   4096 rows    100 / 53.6 / 43.2;                         109 / 83 / 89
 // and more channels than that fill the SMs without.
 template <typename T, typename C>
 bool pick_prefill(const ScanParams& p, int64_t max_rows, int sms, cudaStream_t s) {
@@ -951,8 +955,8 @@ bool launch_prefill(const ScanParams& p, int64_t max_rows, int sms, cudaStream_t
   if (p.size > 32) return pick_prefill<T, Cfg<T, 64, 8>>(p, max_rows, sms, s);
   if (p.size > 16) return pick_prefill<T, Cfg<T, 32, 4>>(p, max_rows, sms, s);
   // Two elements per lane (16 channels a CTA) while that leaves no SM two CTAs, else four (32
-  // channels).  4096 rows of 1024 / 2048 / 2560 channels, us: two 119 / 121 / 198, four 154 /
-  // 159 / 159.
+  // channels).  4096 rows of 1024 / 2048 / 2560 channels, us: two 109 / 107 / 167, four 142 /
+  // 145 / 145.
   if (static_cast<int64_t>(p.seq.num) * p.channels <= 16LL * sms)
     return pick_prefill<T, Cfg<T, 16, 2>>(p, max_rows, sms, s);
   return go_prefill<T, Cfg<T, 16, 4>, 1>(p, sms, s);
