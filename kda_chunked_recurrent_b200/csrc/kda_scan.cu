@@ -22,8 +22,8 @@
 // Measured: 8192 rows of 4096 BF16 channels 285 us, of which the exponentials alone would
 // take 150 at their rate, all special functions 171 (128 of 148 SMs have work); 16 ragged
 // prompts of 2048 FP16 channels 365 us, against 260.  With one scan and one helper warp on a
-// scheduler the rest is latency: a row takes 67 clocks, of which the scan warp's 4
-// exponentials a lane are 33 and the helpers' work on the same units 20.  Tried and dropped, us
+// scheduler the rest is latency: a row takes 67 clocks, where the scan warp's 4
+// exponentials a lane need 32 and the helpers' special functions 5.  Tried and dropped, us
 // for the first: one exponential in eight on the FMA pipe 337 (of 312 then), B and C in FP32
 // and d in pairs in shared memory 306 (of 285; in pairs alone 294), separate warps for staging
 // and writing 283 (of 293), but 386 of 373 for the ragged prompts, two channels per lane 419
