@@ -203,7 +203,8 @@ Conv conv_args(const Tensor& x, PyObject* weight_o, PyObject* bias_o, const Tens
   c.weight = like(&weight, "weight", at::kFloat, {c.ch, c.width}, dev);
   c.bias = like(tensor(bias_o, "bias"), "bias", at::kFloat, {c.ch}, dev);
   if (state != nullptr) {
-    TORCH_CHECK_VALUE(state->dim() == 3, "state: [slots, width - 1, channels] expected");
+    TORCH_CHECK_VALUE(state->dim() == 3 && state->size(0) >= 1,
+                      "state: [slots, width - 1, channels] expected, with a slot at least");
     c.slots = state->size(0);
   }
   c.state = like(state, "state", x.scalar_type(), {c.slots, c.width - 1, c.ch}, dev);
@@ -313,7 +314,8 @@ Scan scan_args(PyObject* const* a) {
   sh.b_stride = rows(B, "B", type, bc, dev, 2);
   sh.c_stride = rows(C, "C", type, bc, dev, 2);
   if (state != nullptr) {
-    TORCH_CHECK_VALUE(state->dim() == 3, "state: [slots, channels, state size] expected");
+    TORCH_CHECK_VALUE(state->dim() == 3 && state->size(0) >= 1,
+                      "state: [slots, channels, state size] expected, with a slot at least");
     sh.pool_size = int32(state->size(0), "slots");
   }
   s.x = x.data_ptr();

@@ -103,6 +103,19 @@ def test_the_library_s_refusals_are_kda_errors():
         K.scan_prefill(x[:, 0], x[:, 0], z(16, 129, dtype=F32), z(2, 1, 129), z(2, 1, 129))
 
 
+def test_a_pool_without_slots_is_refused():
+    """It would otherwise pass for no pool at all: sequences that leave nothing behind."""
+    x, w, A, B = z(8, 16), z(16, 4, dtype=F32), z(16, 4, dtype=F32), z(8, 1, 4)
+    with pytest.raises(ValueError, match="with a slot at least"):
+        K.conv_prefill(x, w, state=z(0, 3, 16))
+    with pytest.raises(ValueError, match="with a slot at least"):
+        K.scan_prefill(x, x, A, B, B, state=z(0, 16, 4, dtype=F32))
+    with pytest.raises(ValueError, match="with a slot at least"):
+        K.conv_decode(x[None], w, z(0, 3, 16))
+    with pytest.raises(ValueError, match="with a slot at least"):
+        K.scan_decode(x[None], x[None], A, B[None], B[None], z(0, 16, 4, dtype=F32))
+
+
 def test_empty_batches():
     """No rows: nothing to write, states as the rules have them."""
     x, w, pool = z(0, 16), z(16, 4, dtype=F32), z(2, 3, 16) + 1
