@@ -148,14 +148,31 @@ Seqs seqs(int64_t n_rows, PyObject* cu_o, PyObject* num_o, const Tensor* state, 
   return s;
 }
 
-// ---- the call: on the tensors' device, its current stream unless one is given
+// ---- the call: on the tensors' device, its current stream unless one is given.  Made before
+// the outputs: they are then allocated on the stream that writes them, as under
+// torch.cuda.stream(); memory of another stream may still be in use there.
+class Call {
+ public:
+  Call(at::Device dev, PyObject* stream) : device_(dev) {
+    if (stream == Py_None) {
+      stream_ = c10::cuda::getCurrentCUDAStream(dev.index()).stream();
+      return;
+    }
+    stream_ = static_cast<cudaStream_t>(PyLong_AsVoidPtr(stream));
+    if (stream_ == nullptr && PyErr_Occurred()) throw python_error();
+    given_.reset_stream(c10::cuda::getStreamFromExternal(stream_, dev.index()));
+  }
+  template <typename F>
+  void launch(const char* where, F&& call) const;
+
+ private:
+  c10::cuda::CUDAGuard device_;
+  c10::cuda::OptionalCUDAStreamGuard given_;
+  cudaStream_t stream_;
+};
 template <typename F>
-void launch(const char* where, at::Device dev, PyObject* stream, F&& call) {
-  const c10::cuda::CUDAGuard guard(dev);
-  void* s = stream == Py_None ? static_cast<void*>(c10::cuda::getCurrentCUDAStream(dev.index()).stream())
-                              : PyLong_AsVoidPtr(stream);
-  if (s == nullptr && PyErr_Occurred()) throw python_error();
-  const kda_status_t rc = call(s);
+void Call::launch(const char* where, F&& call) const {
+  const kda_status_t rc = call(static_cast<void*>(stream_));
   if (rc == KDA_OK) return;
   PyObject* r = PyObject_CallFunction(g_fail, "is", static_cast<int>(rc), where);
   Py_XDECREF(r);
@@ -235,13 +252,14 @@ PyObject* conv_prefill(PyObject*, PyObject* const* a, Py_ssize_t nargs) {
   const Tensor& x = need(a[0], "x");
   TORCH_CHECK_VALUE(x.dim() == 2, "x: [T, C] expected");
   on_gpu(x);
+  const Call call(x.device(), a[12]);
   const Tensor* state = tensor(a[3], "state");
   const Conv c = conv_args(x, a[1], a[2], state, a[8]);
   const Seqs s = seqs(x.size(0), a[6], a[7], state, a[4], a[5], a[11], x.device());
   const kda_conv_shape_t shape = conv_shape(c, s.num, x.size(0), x);
   const Tensor out = output(tensor(a[10], "out"), "out", x.scalar_type(), c.out, x);
   const uint32_t flags = s.flags | (truth(a[9]) ? KDA_CONV_SILU : 0u);
-  launch("kda_conv_prefill", x.device(), a[12], [&](void* stream) {
+  call.launch("kda_conv_prefill", [&](void* stream) {
     return kda_conv_prefill(x.data_ptr(), as<float>(c.weight), as<float>(c.bias), c.state,
                             as<int32_t>(s.slots), as<uint8_t>(s.has), s.cu, &shape,
                             out.data_ptr(), as<int32_t>(s.status), flags, stream);
@@ -258,6 +276,7 @@ PyObject* conv_decode(PyObject*, PyObject* const* a, Py_ssize_t nargs) {
   const Tensor& x = need(a[0], "x");
   TORCH_CHECK_VALUE(x.dim() == 3, "x: [N, T, C] expected");
   on_gpu(x);
+  const Call call(x.device(), a[12]);
   const at::Device dev = x.device();
   const int64_t N = x.size(0), T = x.size(1);
   const Tensor& state = need(a[3], "state");
@@ -272,7 +291,7 @@ PyObject* conv_decode(PyObject*, PyObject* const* a, Py_ssize_t nargs) {
     steps = output(steps_in, "step_states", x.scalar_type(), {N, T, c.width - 1, c.ch}, x);
   const uint32_t flags =
       (truth(a[6]) ? KDA_CONV_SILU : 0u) | (truth(a[10]) ? KDA_LAYER_KEEP_STATE : 0u);
-  launch("kda_conv_decode", dev, a[12], [&](void* stream) {
+  call.launch("kda_conv_decode", [&](void* stream) {
     return kda_conv_decode(x.data_ptr(), as<float>(c.weight), as<float>(c.bias), c.state,
                            as<int32_t>(slots), &shape, out.data_ptr(),
                            steps ? steps->data_ptr() : nullptr, as<int32_t>(status), flags,
@@ -338,6 +357,7 @@ PyObject* scan_prefill(PyObject*, PyObject* const* a, Py_ssize_t nargs) {
   const Tensor& x = need(a[0], "x");
   TORCH_CHECK_VALUE(x.dim() == 2, "x: [T, D] expected");
   on_gpu(x);
+  const Call call(x.device(), a[17]);
   Scan c = scan_args(a);
   const Seqs s = seqs(x.size(0), a[11], a[12], tensor(a[8], "state"), a[9], a[10], a[16],
                       x.device());
@@ -346,7 +366,7 @@ PyObject* scan_prefill(PyObject*, PyObject* const* a, Py_ssize_t nargs) {
   c.shape.max_seqlen = int32(integer(a[13]), "max_seqlen");
   const Tensor out = output(tensor(a[15], "out"), "out", x.scalar_type(), x.sizes(), x);
   const uint32_t flags = s.flags | (truth(a[14]) ? KDA_SCAN_SOFTPLUS : 0u);
-  launch("kda_scan_prefill", x.device(), a[17], [&](void* stream) {
+  call.launch("kda_scan_prefill", [&](void* stream) {
     return kda_scan_prefill(c.x, c.dt, as<float>(c.A_log), c.B, c.C, as<float>(c.D), c.z,
                             as<float>(c.bias), as<float>(c.state), as<int32_t>(s.slots),
                             as<uint8_t>(s.has), s.cu, &c.shape, out.data_ptr(),
@@ -364,6 +384,7 @@ PyObject* scan_decode(PyObject*, PyObject* const* a, Py_ssize_t nargs) {
   const Tensor& x = need(a[0], "x");
   TORCH_CHECK_VALUE(x.dim() == 3, "x: [N, T, D] expected");
   on_gpu(x);
+  const Call call(x.device(), a[16]);
   need(a[8], "state");
   const at::Device dev = x.device();
   const int64_t N = x.size(0), T = x.size(1);
@@ -380,7 +401,7 @@ PyObject* scan_decode(PyObject*, PyObject* const* a, Py_ssize_t nargs) {
                    {N, T, x.size(2), static_cast<int64_t>(c.shape.state_size)}, x);
   const uint32_t flags =
       (truth(a[10]) ? KDA_SCAN_SOFTPLUS : 0u) | (truth(a[14]) ? KDA_LAYER_KEEP_STATE : 0u);
-  launch("kda_scan_decode", dev, a[16], [&](void* stream) {
+  call.launch("kda_scan_decode", [&](void* stream) {
     return kda_scan_decode(c.x, c.dt, as<float>(c.A_log), c.B, c.C, as<float>(c.D), c.z,
                            as<float>(c.bias), as<float>(c.state), as<int32_t>(slots), &c.shape,
                            out.data_ptr(), steps ? as<float>(steps->data_ptr()) : nullptr,
@@ -399,6 +420,7 @@ PyObject* rms_norm(PyObject*, PyObject* const* a, Py_ssize_t nargs) {
   const int dims = static_cast<int>(x.dim()), tail = dims - 1;
   TORCH_CHECK_VALUE(dims == 2 || dims == 3, "x: [T, W] or [T, H, W] expected");
   on_gpu(x);
+  const Call call(x.device(), a[11]);
   const at::Device dev = x.device();
   const at::ScalarType type = x.scalar_type();
   const Tensor *res = tensor(a[3], "residual"), *gate = tensor(a[4], "gate"),
@@ -434,7 +456,7 @@ PyObject* rms_norm(PyObject*, PyObject* const* a, Py_ssize_t nargs) {
     scales = output(scales_in, "scales", at::kFloat, s, x);
   }
   const uint32_t flags = static_cast<uint32_t>(integer(a[5]));
-  launch("kda_rms_norm", dev, a[11], [&](void* stream) {
+  call.launch("kda_rms_norm", [&](void* stream) {
     return kda_rms_norm(x.data_ptr(), as<float>(weight), res ? res->data_ptr() : nullptr,
                         gate ? gate->data_ptr() : nullptr, &sh, out.data_ptr(),
                         res_out ? res_out->data_ptr() : nullptr,

@@ -4,8 +4,9 @@ short causal convolution, selective state space scan and root-mean-square norm.
 Like ``prefill`` and ``decode`` these functions only check and marshal arguments and allocate
 outputs (in the native binding, csrc/kda_layer_bind.cpp); all arithmetic is in the library's
 kernels.  A call is one launch on ``stream`` (the tensors' device's current stream by
-default), reads nothing back and can be captured in a CUDA graph.  Wrong types, shapes, strides
-or devices raise ValueError, what the library refuses raises KDAError.
+default), reads nothing back and can be captured in a CUDA graph.  New outputs are allocated on
+the same stream, as under ``torch.cuda.stream(stream)``.  Wrong types, shapes, strides or devices
+raise ValueError, what the library refuses raises KDAError.
 """
 from __future__ import annotations
 

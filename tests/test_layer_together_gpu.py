@@ -284,3 +284,30 @@ def test_an_explicit_stream_is_used():
     graph.replay()
     torch.cuda.synchronize()
     assert torch.equal(out, want)
+
+
+@pytest.mark.parametrize("call", [
+    lambda K, x, w, s: K.rms_norm(x, stream=s)[0],
+    lambda K, x, w, s: K.conv_prefill(x, w, stream=s),
+], ids=["norm", "conv"])
+def test_outputs_belong_to_the_given_stream(call):
+    """An output is not memory that the current stream has just freed: its work there, which the
+    given stream does not wait for, may not be done."""
+    import kda_chunked_recurrent_b200 as K
+    s = torch.cuda.Stream()
+    x = torch.randn(4099, 1031, device="cuda")     # a size that nothing else has
+    w = torch.ones(1031, 4, device="cuda")
+    torch.cuda.synchronize()
+    freed = torch.empty_like(x)
+    address = freed.data_ptr()
+    del freed
+    again = torch.empty_like(x)
+    assert again.data_ptr() == address             # so the allocator gives it out again
+    del again
+    other = call(K, x, w, s)
+    torch.cuda.synchronize()
+    assert other.data_ptr() != address
+    with torch.cuda.stream(s):
+        same = call(K, x, w, None)
+    torch.cuda.synchronize()
+    assert torch.equal(other, same)
