@@ -58,7 +58,8 @@ struct Vec {
 #pragma unroll
     for (int i = 0; i < kWords; ++i) w[i] = 0u;
   }
-  template <bool kVec>
+  // Not kVec: element by element, kGap apart, those below `count`.
+  template <bool kVec, int kGap = 1>
   __device__ __forceinline__ void load(const typename T::Raw* p, int count = n) {
     if constexpr (kVec) {
       if constexpr (kBytes % 16 == 0) {
@@ -83,15 +84,15 @@ struct Vec {
       clear();
 #pragma unroll
       for (int i = 0; i < n; ++i)
-        if (i < count) {
+        if (i * kGap < count) {
           if constexpr (sizeof(typename T::Raw) == 4)
-            w[i] = __float_as_uint(p[i]);
+            w[i] = __float_as_uint(p[i * kGap]);
           else
-            w[i / 2] |= static_cast<uint32_t>(p[i]) << (16 * (i % 2));
+            w[i / 2] |= static_cast<uint32_t>(p[i * kGap]) << (16 * (i % 2));
         }
     }
   }
-  template <bool kVec>
+  template <bool kVec, int kGap = 1>
   __device__ __forceinline__ void store(typename T::Raw* p, int count = n) const {
     if constexpr (kVec) {
       if constexpr (kBytes % 16 == 0) {
@@ -109,21 +110,22 @@ struct Vec {
     } else {
 #pragma unroll
       for (int i = 0; i < n; ++i)
-        if (i < count) {
+        if (i * kGap < count) {
           if constexpr (sizeof(typename T::Raw) == 4)
-            p[i] = __uint_as_float(w[i]);
+            p[i * kGap] = __uint_as_float(w[i]);
           else
-            p[i] = static_cast<uint16_t>(w[i / 2] >> (16 * (i % 2)));
+            p[i * kGap] = static_cast<uint16_t>(w[i / 2] >> (16 * (i % 2)));
         }
     }
   }
-  // In pieces of kStep elements that lie whole within `count` or behind it (kStep = 1: any).
-  template <int kStep>
+  // In pieces of kStep elements that lie whole within `count` or behind it (kStep = 1: any,
+  // kGap apart).
+  template <int kStep, int kGap = 1>
   __device__ __forceinline__ void load_by(const typename T::Raw* p, int count) {
     if constexpr (kStep == n) {
       load<true>(p);
     } else if constexpr (kStep == 1) {
-      load<false>(p, count);
+      load<false, kGap>(p, count);
     } else {
 #pragma unroll
       for (int i = 0; i < n / kStep; ++i) {
@@ -135,12 +137,12 @@ struct Vec {
       }
     }
   }
-  template <int kStep>
+  template <int kStep, int kGap = 1>
   __device__ __forceinline__ void store_by(typename T::Raw* p, int count) const {
     if constexpr (kStep == n) {
       store<true>(p);
     } else if constexpr (kStep == 1) {
-      store<false>(p, count);
+      store<false, kGap>(p, count);
     } else {
 #pragma unroll
       for (int i = 0; i < n / kStep; ++i) {
