@@ -9,8 +9,8 @@
 // one load, two reductions and one store for few.  r is not rounded before the norm (the
 // stored residual is its rounding): one rounding fewer than norming the stored sum.
 // 8192 rows of 4096 BF16 with residual: 43.4 us, 6.2 TB/s; 393216 rows of 128 with gate, in
-// E4M3: 56 us, 4.5 TB/s, there bound by issued instructions (25 an element and warp, two
-// special functions for the gate among them).
+// E4M3: 49.6 us, 5.1 TB/s, there bound by issued instructions, two special functions an element
+// for the gate among them.
 //
 // kTPR threads share a row: a part of a warp for short rows (the heads of a token: no
 // barrier at all), several warps for long ones (one barrier per reduction).  A thread holds
@@ -58,9 +58,9 @@ __device__ __forceinline__ float row_reduce(float v, float* smem, int row_in_cta
 
 // kStep: elements that are moved at a time: 8 (the width is a multiple of 8, all rows lie on 16
 // bytes), 4 (the same with 4 and half the bytes) or 1.  kR rows per thread: short rows share
-// the weights and the reckoning of addresses.
-template <typename T, int kTPR, int kChunks, int kThreads, int kR, int kStep>
-__global__ void __launch_bounds__(kThreads) kda_rms_norm_kernel(const NormParams p) {
+// the weights and the reckoning of addresses.  kMin: CTAs an SM has to hold (0: no rule).
+template <typename T, int kTPR, int kChunks, int kThreads, int kR, int kStep, int kMin>
+__global__ void __launch_bounds__(kThreads, kMin) kda_rms_norm_kernel(const NormParams p) {
   using Raw = typename T::Raw;
   static_assert(kThreads % kTPR == 0, "whole rows");
   static_assert(kR == 1 || kTPR <= 32, "one row per thread where warps share it");
@@ -276,15 +276,19 @@ __global__ void __launch_bounds__(kThreads) kda_rms_norm_kernel(const NormParams
   }
 }
 
-template <typename T, int kTPR, int kChunks, int kThreads, int kR = 1>
-bool go(const NormParams& p, cudaStream_t s) {
+template <typename T, int kTPR, int kChunks, int kThreads, int kR, int kStep, int kMin = 0>
+bool go_step(const NormParams& p, cudaStream_t s) {
   const int64_t per = kThreads / kTPR * kR, grid = (p.rows + per - 1) / per;
   if (grid > INT32_MAX) return false;
-  const auto kernel = p.step == 8   ? kda_rms_norm_kernel<T, kTPR, kChunks, kThreads, kR, 8>
-                      : p.step == 4 ? kda_rms_norm_kernel<T, kTPR, kChunks, kThreads, kR, 4>
-                                    : kda_rms_norm_kernel<T, kTPR, kChunks, kThreads, kR, 1>;
-  kernel<<<static_cast<unsigned>(grid), kThreads, 0, s>>>(p);
+  kda_rms_norm_kernel<T, kTPR, kChunks, kThreads, kR, kStep, kMin>
+      <<<static_cast<unsigned>(grid), kThreads, 0, s>>>(p);
   return true;
+}
+template <typename T, int kTPR, int kChunks, int kThreads, int kR = 1>
+bool go(const NormParams& p, cudaStream_t s) {
+  if (p.step == 8) return go_step<T, kTPR, kChunks, kThreads, kR, 8>(p, s);
+  if (p.step == 4) return go_step<T, kTPR, kChunks, kThreads, kR, 4>(p, s);
+  return go_step<T, kTPR, kChunks, kThreads, kR, 1>(p, s);
 }
 
 template <typename T>
@@ -293,7 +297,15 @@ bool launch(NormParams p, cudaStream_t s) {
   const int W = p.width;
   if (W <= 128) p.group = 0;      // one scale group: the row
   if (W <= 64) return go<T, 8, 1, 128, 4>(p, s);
-  if (W <= 128) return go<T, 16, 1, 128, 4>(p, s);
+  // Rows of 65 to 128: two chunks a thread, which spend less on addresses and sums than one, in
+  // 64 registers (393216 rows of 128 with gate in E4M3, us: 49.6; 51.5 without that limit; one
+  // chunk of four rows 55.9, of two 61).  Element by element one chunk is better (48000 rows of
+  // 125: 14.6 against 18.4).
+  if (W <= 128) {
+    if (p.step == 8) return go_step<T, 8, 2, 128, 2, 8, 8>(p, s);
+    if (p.step == 4) return go_step<T, 8, 2, 128, 2, 4, 8>(p, s);
+    return go_step<T, 16, 1, 128, 2, 1>(p, s);
+  }
   if (W <= 256) return go<T, 32, 1, 128, 2>(p, s);
   if (W <= 512) return go<T, 32, 2, 128>(p, s);
   if (W <= 1024) return go<T, 128, 1, 128>(p, s);
