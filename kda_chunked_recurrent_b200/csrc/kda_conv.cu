@@ -292,7 +292,7 @@ __global__ void __launch_bounds__(256) kda_conv_decode_kernel(const ConvParams p
   Vec<T, kV> win[kSeqs][W];
 #pragma unroll
   for (int i = 0; i < kSeqs; ++i)
-    slot[i] = n0 + i < p.seq.num ? state_slot(p.slot, n0 + i, p.pool, p.status, c0 == 0) : -2;
+    slot[i] = n0 + i < p.seq.num ? state_slot(p.slot, n0 + i, p.pool, p.status, c0 == 0) : -1;
   const Raw* x = static_cast<const Raw*>(p.x) + c0;
 #pragma unroll
   for (int i = 0; i < kSeqs; ++i) {
@@ -312,7 +312,7 @@ __global__ void __launch_bounds__(256) kda_conv_decode_kernel(const ConvParams p
 #pragma unroll
   for (int i = 0; i < kSeqs; ++i) {
     const int64_t row0 = static_cast<int64_t>(n0 + i) * T_new;
-    if (slot[i] == -2) break;
+    if (n0 + i >= p.seq.num) break;
     if (slot[i] < 0) {   // a padding row: zero outputs
       const float zero[kV] = {};
       for (int32_t t = 0; t < T_new; ++t) out.put(row0 + t, zero);

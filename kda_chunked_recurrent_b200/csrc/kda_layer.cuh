@@ -230,7 +230,7 @@ __device__ __forceinline__ int32_t state_slot(const int32_t* idx, int32_t n, int
     if (reports && status != nullptr) atomicCAS(status, 0, kStatusBadIndex);
     return -1;
   }
-  return i;
+  return max(i, -1);
 }
 
 // ---- kernel parameters ---------------------------------------------------------------
