@@ -117,7 +117,8 @@ kda_status_t kda_conv_decode(const void* x, const float* weight, const float* bi
  *   h[c,n] <- exp(d A[c,n]) h[c,n] + d B[t,g,n] x[t,c]
  *   y       = sum_n C[t,g,n] h[c,n] + D[c] x[t,c]
  *   out     = y z[t,c] / (1 + exp(-z[t,c]))   (without z: y)
- * Channels are dealt to the groups in equal runs.  The state is FP32.
+ * Channels are dealt to the groups in equal runs.  The state is FP32.  A_log may be any
+ * number: -infinity is a rate of zero (no decay), and rates above 2.3e38 count as that.
  */
 typedef struct {
   int32_t num_seqs;    /* N >= 1                                                         */

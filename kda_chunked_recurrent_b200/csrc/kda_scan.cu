@@ -63,13 +63,18 @@ __device__ __forceinline__ void copy_wait() {
   asm volatile("cp.async.wait_group %0;" ::"n"(kPending) : "memory");
 }
 
-// e^v with the rounding of v log2(e) made good: the product's error times ln 2 is added to the
-// result relatively, so that a decay rate is off by no more than the exponential's own 2^-22.
-__device__ __forceinline__ float ex2_full(float v) {
+// -log2(e) e^v, the decay rate of A_log = v in powers of two.  The rounding of v log2(e) is made
+// good: the product's error times ln 2 is added to the exponential relatively, so that a rate is
+// off by no more than the exponential's own 2^-22.  Where the product is infinite or far down
+// there is no such error to take (infinity less infinity), and near 2^128 the rate leaves FP32
+// anyway: it is held at the largest number, so that a step of zero behind it still decays
+// nothing.  v = -infinity gives a rate of zero.
+__device__ __forceinline__ float decay_rate(float v) {
   const float y = v * kLog2e;
   const float e = fmaf(v, kLog2e, -y) + v * 1.925963033500948e-8f;   // log2(e) - its FP32 value
-  const float r = ex2(y);
-  return fmaf(r, e * 0.6931471805599453f, r);
+  float r = ex2(y);
+  if (y > -150.f && y < 127.75f) r = fmaf(r, e * 0.6931471805599453f, r);
+  return max_nan(-kLog2e * r, -3.402823466e38f);
 }
 
 // All threads of a cluster: what was written before the arrival is seen after the wait.
@@ -361,7 +366,7 @@ __global__ void __launch_bounds__(kThreads, 2) kda_scan_prefill_kernel(const Sca
     for (int i = 0; i < C::kS; ++i) {
       const bool in = ch < nch && q * C::kS + i < p.size;
       // elements past the state's size decay at rate 0 and take nothing: B and C are 0 there
-      A[i] = in ? -kLog2e * ex2_full(p.A_log[at + i]) : 0.f;
+      A[i] = in ? decay_rate(p.A_log[at + i]) : 0.f;
       const float v = (in && old) ? state[i] : 0.f;
       if (i % 2 == 0) h[i / 2].x = v;
       else h[i / 2].y = v;
@@ -682,7 +687,7 @@ kda_scan_token_kernel(const ScanParams p) {
       float a[4];
       av.unpack(a);
 #pragma unroll
-      for (int i = 0; i < 4; ++i) a[i] = i < count ? -kLog2e * ex2_full(a[i]) : 0.f;
+      for (int i = 0; i < 4; ++i) a[i] = i < count ? decay_rate(a[i]) : 0.f;
       A[0] = make_float2(a[0], a[1]);
       A[1] = make_float2(a[2], a[3]);
       bias = p.dt_bias != nullptr ? p.dt_bias[c] : 0.f;

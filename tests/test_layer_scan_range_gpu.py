@@ -1,0 +1,104 @@
+"""The scan at the ends of the range: decay rates of zero and without end (needs a B200)."""
+import numpy as np
+import pytest
+import torch
+
+import kda_chunked_recurrent_b200 as K
+from tests.layer_reference import close, f64, scan
+
+pytestmark = pytest.mark.gpu
+INF, NAN = float("inf"), float("nan")
+
+# (lengths, channels): blocks with rows behind the last; rows shared by several thread blocks;
+# many prompts of few rows
+FORMS = {"blocks": ([45, 3, 32], 24), "shared": ([700], 24), "few rows": ([16, 5, 1] + [9] * 17, 1024)}
+
+
+def _inputs(rows, D, S, seed):
+    g = torch.Generator().manual_seed(seed)
+    r = lambda *s: torch.randn(*s, generator=g)  # noqa: E731
+    x, z, B, C = r(rows, D).cuda(), r(rows, D).cuda(), r(rows, 1, S).cuda(), r(rows, 1, S).cuda()
+    dt = torch.exp(-5 + 2 * torch.rand(rows, D, generator=g)).cuda()     # steps of 0.007 to 0.05
+    return x, dt, z, B, C, r(D).cuda(), g
+
+
+def _prompts(lens, x, dt, A_log, B, C, pool, **kw):
+    cu = torch.tensor(np.concatenate([[0], np.cumsum(lens)]), dtype=torch.int32, device="cuda")
+    return K.scan_prefill(x, dt, A_log, B, C, state=pool, cu_seqlens=cu, max_seqlen=max(lens),
+                          softplus=False, **kw)
+
+
+# rates of zero (what log(0) gives), far below and above the usual, and beyond FP32
+RATES = [-INF, -3.0e38, -1.0e30, -200.0, -90.0, 0.0, 88.0, 88.5, 88.7, 88.75, 89.0, 89.25, 90.5,
+         93.0, 97.0, 101.0, 110.0, 300.0]
+
+
+def _rates(D, S, g):
+    A_log = torch.randn(D, S, generator=g)
+    for i, v in enumerate(RATES):
+        A_log[i % D, (3 * i) % S] = v
+        A_log[D - 1 - i % D, 0] = v
+    return A_log.cuda()
+
+
+@pytest.mark.parametrize("S", [13, 16, 128])
+@pytest.mark.parametrize("form", list(FORMS))
+def test_rates_of_prompts(form, S):
+    lens, D = FORMS[form]
+    x, dt, z, B, C, skip, g = _inputs(sum(lens), D, S, S)
+    A_log = _rates(D, S, g)
+    pool = torch.randn(len(lens), D, S, generator=g).cuda()
+    before = f64(pool)
+    out = _prompts(lens, x, dt, A_log, B, C, pool, D=skip, z=z)
+    torch.cuda.synchronize()
+    a = 0
+    for n, L in enumerate(lens):
+        cut = lambda t: f64(t[a:a + L])  # noqa: E731
+        y, yb, hs, es = scan(cut(x), cut(dt), f64(A_log), cut(B), cut(C), f64(skip), cut(z), None,
+                             before[n], False)
+        close(out[a:a + L], y, yb, torch.float32, f"rows of sequence {n}")
+        close(pool[n], hs[-1], es[-1], torch.float32, f"state of sequence {n}")
+        a += L
+
+
+@pytest.mark.parametrize("S", [13, 16, 128])
+@pytest.mark.parametrize("T", [1, 4])
+def test_rates_of_tokens(T, S):
+    N, D = 5, 24
+    x, dt, z, B, C, skip, g = _inputs(N * T, D, S, S + T)
+    A_log = _rates(D, S, g)
+    pool = torch.randn(N, D, S, generator=g).cuda()
+    before = f64(pool)
+    f = lambda t: t.unflatten(0, (N, T))  # noqa: E731
+    out = K.scan_decode(f(x), f(dt), A_log, f(B), f(C), pool, D=skip, z=f(z), softplus=False)[0]
+    torch.cuda.synchronize()
+    for n in range(N):
+        cut = lambda t: f64(t[n * T:(n + 1) * T])  # noqa: E731
+        y, yb, hs, es = scan(cut(x), cut(dt), f64(A_log), cut(B), cut(C), f64(skip), cut(z), None,
+                             before[n], False)
+        close(out[n], y, yb, torch.float32, f"rows of sequence {n}")
+        close(pool[n], hs[-1], es[-1], torch.float32, f"state of sequence {n}")
+
+
+@pytest.mark.parametrize("beyond", [3.0e38, INF])
+def test_rates_beyond_the_range_forget_all(beyond):
+    """As any rate whose decay is 0; a rate that is NaN stays one."""
+    lens, D, S = [45, 3], 24, 16
+    x, dt, z, B, C, skip, g = _inputs(48, D, S, 1)
+    pool = torch.randn(2, D, S, generator=g).cuda()
+    A_log = torch.zeros(D, S, device="cuda")
+    got, want = [], []
+    for into, v in ((got, beyond), (want, 300.0)):
+        A_log[3] = v
+        state = pool.clone()
+        into += [_prompts(lens, x, dt, A_log, B, C, state), state]
+        state = pool.clone()
+        into += [K.scan_decode(x[:2, None], dt[:2, None], A_log, B[:2, None], C[:2, None], state,
+                               softplus=False)[0], state]
+    for a, b in zip(got, want):
+        assert torch.equal(a, b) and torch.isfinite(a).all()
+    A_log[3] = NAN
+    state = pool.clone()
+    out = _prompts(lens, x, dt, A_log, B, C, state)
+    assert torch.isnan(out[:, 3]).all() and torch.isnan(state[:, 3]).all()
+    assert torch.isnan(out).sum() == 48 and torch.isnan(state).sum() == 2 * S
