@@ -97,8 +97,9 @@ __device__ __forceinline__ float2 splat(float v) { return make_float2(v, v); }
 __device__ __forceinline__ float2 softplus2(float2 v) {
   const float2 e = make_float2(ex2(-fabsf(v.x) * kLog2e), ex2(-fabsf(v.y) * kLog2e));
   const float2 t = add2<true>(e, splat(2.f));
-  const float r2 = rcp_approx(t.x * t.y);      // both reciprocals from one (2 <= t <= 3)
-  const float2 s = mul2<true>(e, make_float2(r2 * t.y, r2 * t.x));
+  // (two reciprocals: the values are of two rows, and one reciprocal of the product would let a
+  // later row, a NaN there above all, into an earlier one)
+  const float2 s = mul2<true>(e, make_float2(rcp_approx(t.x), rcp_approx(t.y)));
   const float2 q = mul2<true>(s, s);
   float2 r = fma2<true>(q, splat(1.f / 13.f), splat(1.f / 11.f));
   r = fma2<true>(q, r, splat(1.f / 9.f));

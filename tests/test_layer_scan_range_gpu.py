@@ -1,4 +1,5 @@
-"""The scan at the ends of the range: decay rates of zero and without end (needs a B200)."""
+"""The scan at the ends of the range: decay rates of zero and without end, steps that
+are not finite (needs a B200)."""
 import numpy as np
 import pytest
 import torch
@@ -102,3 +103,43 @@ def test_rates_beyond_the_range_forget_all(beyond):
     out = _prompts(lens, x, dt, A_log, B, C, state)
     assert torch.isnan(out[:, 3]).all() and torch.isnan(state[:, 3]).all()
     assert torch.isnan(out).sum() == 48 and torch.isnan(state).sum() == 2 * S
+
+
+@pytest.mark.parametrize("dtype", [torch.bfloat16, torch.float32])
+@pytest.mark.parametrize("form", list(FORMS))
+@pytest.mark.parametrize("at", [2, 3])
+@pytest.mark.parametrize("value", [NAN, INF])
+def test_a_step_that_is_not_finite_leaves_the_rows_before_it(form, dtype, at, value):
+    """A NaN or an infinity in dt, at an even and at an odd row: the rows before it, the other
+    channels and the other sequences are what they are without it."""
+    lens, D = FORMS[form]
+    x, dt, z, B, C, skip, g = _inputs(sum(lens), D, 16, 5)
+    x, dt, z, B, C = (t.to(dtype) for t in (x, dt, z, B, C))
+    A_log = torch.zeros(D, 16, device="cuda")
+    cu = torch.tensor(np.concatenate([[0], np.cumsum(lens)]), dtype=torch.int32, device="cuda")
+    runs = []
+    for v in (None, value):
+        if v is not None:
+            dt = dt.clone()
+            dt[at, 5] = v
+        pool = torch.zeros(len(lens), D, 16, device="cuda")
+        runs.append((K.scan_prefill(x, dt, A_log, B, C, D=skip, z=z, state=pool, cu_seqlens=cu,
+                                    max_seqlen=max(lens)), pool))
+    (y, p), (yn, pn) = runs
+    hit = torch.zeros_like(y, dtype=torch.bool)
+    hit[at:lens[0], 5] = True
+    assert torch.equal(y[~hit], yn[~hit]) and not torch.isfinite(yn[hit]).any()
+    assert torch.isfinite(y).all() and not torch.isfinite(pn[0, 5]).any()
+    pn[0, 5] = p[0, 5]
+    assert torch.equal(p, pn)
+
+
+def test_a_step_that_is_nan_in_tokens():
+    x, dt, z, B, C, skip, g = _inputs(6, 24, 16, 6)
+    f = lambda t: t.unflatten(0, (2, 3))  # noqa: E731
+    dt[1, 5] = NAN
+    pool = torch.zeros(2, 24, 16, device="cuda")
+    out = K.scan_decode(f(x), f(dt), torch.zeros(24, 16, device="cuda"), f(B), f(C), pool)[0]
+    bad = torch.isnan(out)
+    assert bad[0, 1:, 5].all() and bad.sum() == 2
+    assert torch.isnan(pool[0, 5]).all() and torch.isnan(pool).sum() == 16
