@@ -119,6 +119,8 @@ kda_status_t kda_conv_decode(const void* x, const float* weight, const float* bi
  *   out     = y z[t,c] / (1 + exp(-z[t,c]))   (without z: y)
  * Channels are dealt to the groups in equal runs.  The state is FP32.  A_log may be any
  * number: -infinity is a rate of zero (no decay), and rates above 2.3e38 count as that.
+ * A row's factor exp(d A) is an FP32 number: a negative step (without softplus) that takes it
+ * above e^88 gives infinities, and a NaN where the state is zero.
  */
 typedef struct {
   int32_t num_seqs;    /* N >= 1                                                         */

@@ -77,6 +77,15 @@ __device__ __forceinline__ float decay_rate(float v) {
   return max_nan(-kLog2e * r, -3.402823466e38f);
 }
 
+// 2^y h + h0 where 2^y may leave FP32's range though the sum does not: then in three factors,
+// held so far out that any number times all three is zero or infinite.  A zero stays zero and an
+// infinity infinite, as row by row.
+__device__ __forceinline__ float carry(float y, float h, float h0) {
+  if (!(fabsf(y) > 126.f)) return fmaf(ex2(y), h, h0);
+  const float f = ex2(fminf(fmaxf(y, -378.f), 378.f) * (1.f / 3.f));
+  return fmaf(f, f * h * f, h0);
+}
+
 // All threads of a cluster: what was written before the arrival is seen after the wait.
 __device__ __forceinline__ void cluster_arrive() { asm volatile("barrier.cluster.arrive;" ::: "memory"); }
 __device__ __forceinline__ void cluster_wait() { asm volatile("barrier.cluster.wait;" ::: "memory"); }
@@ -396,9 +405,8 @@ __global__ void __launch_bounds__(kThreads, 2) kda_scan_prefill_kernel(const Sca
 #pragma unroll
         for (int i = 0; i < Ops<C>::kP; ++i) {
           const float2 y = mul2<true>(splat(d), make_float2(A[2 * i], A[2 * i + 1]));
-          h[i] = fma2<true>(make_float2(ex2(y.x), ex2(y.y)), h[i],
-                            make_float2(cluster_load(&ex.h[tid][2 * i], j),
-                                        cluster_load(&ex.h[tid][2 * i + 1], j)));
+          h[i].x = carry(y.x, h[i].x, cluster_load(&ex.h[tid][2 * i], j));
+          h[i].y = carry(y.y, h[i].y, cluster_load(&ex.h[tid][2 * i + 1], j));
         }
       }
       cluster_arrive();     // the neighbours' shared memory is not looked at any more

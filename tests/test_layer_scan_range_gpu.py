@@ -1,5 +1,5 @@
 """The scan at the ends of the range: decay rates of zero and without end, steps that
-are not finite (needs a B200)."""
+are not finite, steps below zero (needs a B200)."""
 import numpy as np
 import pytest
 import torch
@@ -143,3 +143,79 @@ def test_a_step_that_is_nan_in_tokens():
     bad = torch.isnan(out)
     assert bad[0, 1:, 5].all() and bad.sum() == 2
     assert torch.isnan(pool[0, 5]).all() and torch.isnan(pool).sum() == 16
+
+
+# Rows shared by several thread blocks: a run of rows is one factor there.  With negative steps
+# (no softplus) that factor may leave FP32's range where the states do not.
+@pytest.mark.parametrize("S,dtype", [(16, torch.float32), (13, torch.bfloat16), (64, torch.float32),
+                                     (128, torch.float32)])
+def test_shared_rows_growth_of_nothing(S, dtype):
+    """700 rows of growth in channels without input before them: the states stay zero."""
+    rows, D = 1100, 24
+    x, dt, z, B, C, skip, g = _inputs(rows, D, S, 7)
+    dt[:700] *= -20            # -0.13 to -1 a row; rates of 1 to S
+    x[:700] = 0
+    x[:, 3] = 0                # and one channel without any
+    x, dt, B, C = (t.to(dtype) for t in (x, dt, B, C))
+    A_log = torch.log(torch.arange(1, S + 1).float()).repeat(D, 1).cuda()
+    pool = torch.zeros(1, D, S, device="cuda")
+    out = K.scan_prefill(x, dt, A_log, B, C, D=skip, state=pool, softplus=False)
+    y, yb, hs, es = scan(f64(x[700:]), f64(dt[700:]), f64(A_log), f64(B[700:]), f64(C[700:]),
+                         f64(skip), None, None, np.zeros((D, S)), False)
+    # A single row's factor is an FP32 number: e^89 is above 2^128, infinite, and infinity times a
+    # zero state has no value.  So elements whose factors all lie below e^88 have to be right, and
+    # the rows of channels without others (with 128 elements a step of 1 takes the last to e^128).
+    fits = f64(-dt).max(0)[:, None] * np.exp(f64(A_log)) < 88
+    rows_fit = fits.all(1)
+    assert fits.sum() >= D * min(S, 80) and (S == 128 or rows_fit.all())
+    ok = torch.tensor(rows_fit).cuda()
+    assert torch.all(out[:700, ok] == 0) and (not ok[3] or torch.all(out[:, 3] == 0))
+    state = f64(pool[0])
+    assert np.all(state[3][fits[3]] == 0)
+    close(out[700:, ok], y[:, rows_fit], yb[:, rows_fit], dtype, "rows")
+    close(state[fits], hs[-1][fits], es[-1][fits], torch.float32, "state")
+
+
+def test_shared_rows_growth_of_little():
+    """A state of 1e-37 grown by e^112 in one run of rows, and decayed by e^-112 behind it."""
+    rows, D, S = 1280, 24, 16       # eight runs of 160 rows
+    x, dt, z, B, C, skip, g = _inputs(rows, D, S, 8)
+    dt[:] = 0.01
+    dt[:160], dt[160:320], dt[320:480] = -0.7, 0.7, -0.35
+    x[:480] = 0
+    pool = 1e-37 * torch.randn(1, D, S, generator=g).cuda()
+    before = f64(pool[0])
+    A_log = torch.zeros(D, S, device="cuda")
+    out = K.scan_prefill(x, dt, A_log, B, C, D=skip, state=pool, softplus=False)
+    y, yb, hs, es = scan(f64(x), f64(dt), f64(A_log), f64(B), f64(C), f64(skip), None, None, before,
+                         False)
+    close(out, y, yb, torch.float32, "rows")
+    close(pool[0], hs[-1], es[-1], torch.float32, "state")
+
+
+def test_shared_rows_bounded_negative_steps():
+    """Steps of both signs whose sums stay small: states of usual size throughout."""
+    rows, D, S = 1500, 40, 16
+    x, dt, z, B, C, skip, g = _inputs(rows, D, S, 9)
+    dt = 0.3 * torch.randn(rows, D, generator=g).cuda()
+    dt -= torch.cat([torch.zeros(1, D, device="cuda"), dt[:-1]])      # steps whose sums stay small
+    pool = torch.randn(1, D, S, generator=g).cuda()
+    before = f64(pool[0])
+    A_log = torch.zeros(D, S, device="cuda")
+    out = K.scan_prefill(x, dt, A_log, B, C, D=skip, z=z, state=pool, softplus=False)
+    y, yb, hs, es = scan(f64(x), f64(dt), f64(A_log), f64(B), f64(C), f64(skip), f64(z), None, before,
+                         False)
+    assert np.abs(hs).max() < 2.0 ** 40          # far from where nothing is asked
+    close(out, y, yb, torch.float32, "rows")
+    close(pool[0], hs[-1], es[-1], torch.float32, "state")
+
+
+def test_shared_rows_keep_an_infinite_state():
+    """As row by row: decays above zero leave an infinity what it is."""
+    rows, D, S = 2048, 24, 16
+    x, dt, z, B, C, skip, g = _inputs(rows, D, S, 10)
+    dt[:] = 0.5
+    pool = torch.randn(1, D, S, generator=g).cuda()
+    pool[0, 4, 7] = INF
+    K.scan_prefill(x, dt, torch.zeros(D, S, device="cuda"), B, C, state=pool, softplus=False)
+    assert pool[0, 4, 7] == INF and torch.isfinite(pool).sum() == D * S - 1
