@@ -5,7 +5,8 @@
  *   - tensor pointers are DEVICE pointers on the current CUDA device, owned by the
  *     caller; no call allocates, keeps a pointer or synchronises the host;
  *   - all work of a call is one launch on `stream` and can be captured in a CUDA graph;
- *   - host-side validation happens before the launch; on an error nothing was enqueued;
+ *   - host-side validation happens before the launch; on an error nothing was enqueued (work of
+ *     more thread blocks than a launch may have, 2^31 - 1, is a bad shape);
  *   - cu_seqlens and slot indices are never read on the host.  The kernels clamp them so
  *     that every address stays in bounds; rows outside [cu_seqlens[0], cu_seqlens[N])
  *     (a padded batch) are neither read into a result nor written.

@@ -11,6 +11,7 @@
 
 namespace kda {
 namespace layer {
+// false: more thread blocks than a launch may have (an error of the launch is CUDA's last error)
 bool launch_conv_prefill(const ConvParams& p, int W, int dtype, int sms, cudaStream_t s);
 bool launch_conv_decode(const ConvParams& p, int W, int dtype, int sms, cudaStream_t s);
 bool launch_scan_prefill(const ScanParams& p, int64_t max_rows, int dtype, int sms,
@@ -70,12 +71,14 @@ struct NvtxRange {
   NvtxRange& operator=(const NvtxRange&) = delete;
 };
 
+// f launches and says whether the work fits one launch; where it does not, nothing was enqueued.
 template <typename F>
 kda_status_t launch(const char* name, F&& f) {
   NvtxRange nr(name);
   (void)cudaGetLastError();
-  const bool ok = f();
-  return ok && cudaGetLastError() == cudaSuccess ? KDA_OK : KDA_ERR_LAUNCH_FAILED;
+  const bool fits = f();
+  if (cudaGetLastError() != cudaSuccess) return KDA_ERR_LAUNCH_FAILED;
+  return fits ? KDA_OK : KDA_ERR_BAD_SHAPE;
 }
 
 // Sequence arguments that conv and scan share.  Decode calls (cu = NULL, per_seq rows each)
