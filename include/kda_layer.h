@@ -25,6 +25,8 @@
  * (scan states and their step_states lie on 16 bytes); 16-byte aligned rows whose length is
  * a multiple of 16 bytes are the fast case.
  *
+ * Counts of rows, of sequences and of a token's elements end at 2^31 - 4097.
+ *
  * Not finite values: an infinity or a NaN stays in the windows, the channel's states or the
  * row that it is in; the SiLU of minus infinity is a NaN.
  */

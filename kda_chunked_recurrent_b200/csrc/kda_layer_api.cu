@@ -46,6 +46,10 @@ bool overlap(const Range& a, std::initializer_list<Range> rs) {
 }
 bool aligned(const void* p, size_t a) { return reinterpret_cast<uintptr_t>(p) % a == 0; }
 
+// The kernels count rows, sequences, heads and the elements of a token in 32 bits, and may look a
+// block's worth past the last before they find that it is not there.
+constexpr int64_t kMost = INT32_MAX - 4096;
+
 int elem_size(int dtype) { return dtype == KDA_DTYPE_F32 ? 4 : 2; }
 bool activation_type(int dtype) { return dtype >= KDA_DTYPE_BF16 && dtype <= KDA_DTYPE_F32; }
 // 16-byte rows: the fast path of the row kernels
@@ -92,8 +96,7 @@ struct SeqArgs {
 };
 kda_status_t check_seqs(const SeqArgs& a, int64_t num, int64_t rows, int64_t pool, bool state,
                         bool decode) {
-  if (num < 1 || rows < 0 || num > INT32_MAX - 1) return KDA_ERR_BAD_SHAPE;
-  if (rows > INT32_MAX - 4096) return KDA_ERR_BAD_SHAPE;   // 32-bit row numbers in the kernels
+  if (num < 1 || rows < 0 || num > kMost || rows > kMost) return KDA_ERR_BAD_SHAPE;
   if (a.cu64 && a.cu == nullptr) return KDA_ERR_BAD_OPTION;
   if (!decode && a.cu == nullptr && rows % num != 0) return KDA_ERR_BAD_SHAPE;
   if (state && (pool < 1 || (a.slot == nullptr && pool < num))) return KDA_ERR_BAD_SHAPE;
@@ -317,7 +320,7 @@ kda_status_t kda_rms_norm(const void* x, const float* weight, const void* residu
       !std::isfinite(sh.eps))
     return KDA_ERR_BAD_OPTION;
   const int64_t T = sh.tokens, H = sh.heads, W = sh.width, most = int64_t(1) << 40;
-  if (T < 0 || H < 1 || W < 1 || W > 32768 || H * W > INT32_MAX) return KDA_ERR_BAD_SHAPE;
+  if (T < 0 || H < 1 || W < 1 || W > 32768 || H * W > kMost) return KDA_ERR_BAD_SHAPE;
   if (sh.x_stride < H * W || sh.x_stride > most ||
       (residual && (sh.residual_stride < H * W || sh.residual_stride > most)) ||
       (residual_out && (sh.residual_out_stride < H * W || sh.residual_out_stride > most)) ||
