@@ -218,8 +218,14 @@ __global__ void __launch_bounds__(kThreads, kMin) kda_rms_norm_kernel(const Norm
     return;
   }
 
-  // 8 bits.  The scale and the factor 1 / scale are products with rounded constants and the
-  // reciprocal approximation: within 2^-22 of the quotients.
+  // 8 bits.  Scale and value / scale are the quotients, rounded once: estimate, what it leaves of
+  // the dividend, and that times the reciprocal on top.  (With products by 448 / max, within 2^-22,
+  // codes next to a border of E4M3 went to the other side.)
+  const auto quotient_448 = [](float amax) {
+    const float q = amax * (1.f / kE4m3Max);
+    const float r = fmaf(fmaf(-q, kE4m3Max, amax), 1.f / kE4m3Max, q);
+    return fabsf(amax) < INFINITY ? r : amax;
+  };
   const auto amax_of = [&](int r, int i) {
     float m = max_nan(fabsf(y[r][i][0].x), fabsf(y[r][i][0].y));
 #pragma unroll
@@ -230,35 +236,40 @@ __global__ void __launch_bounds__(kThreads, kMin) kda_rms_norm_kernel(const Norm
 #pragma unroll
   for (int r = 0; r < kR; ++r) {
     const int64_t row = first + r * kRows + ric;
-    float factor[kChunks];
+    float scale[kChunks];
     if (p.group == 0) {
       float m = amax_of(r, 0);
 #pragma unroll
       for (int i = 1; i < kChunks; ++i) m = max_nan(m, amax_of(r, i));
       const float amax = max_nan(row_reduce<kTPR, kThreads, true>(m, s_max, ric), kAmaxFloor);
-      if (n[r] > 0 && j == 0) p.scales[row] = amax * (1.f / kE4m3Max);
+      const float sc = quotient_448(amax);
+      if (n[r] > 0 && j == 0) p.scales[row] = sc;
 #pragma unroll
-      for (int i = 0; i < kChunks; ++i) factor[i] = kE4m3Max * rcp_approx(amax);
+      for (int i = 0; i < kChunks; ++i) scale[i] = sc;
     } else if constexpr (kTPR % 16 == 0) {     // (shorter rows are one group)
 #pragma unroll
       for (int i = 0; i < kChunks; ++i) {
         float m = amax_of(r, i);
 #pragma unroll
         for (int o = 8; o > 0; o >>= 1) m = max_nan(m, __shfl_xor_sync(0xffffffffu, m, o));
-        const float amax = max_nan(m, kAmaxFloor);
+        scale[i] = quotient_448(max_nan(m, kAmaxFloor));
         if (left(r, i) > 0 && (j & 15) == 0)
-          p.scales[row * p.groups + (j + i * kTPR) / 16] = amax * (1.f / kE4m3Max);
-        factor[i] = kE4m3Max * rcp_approx(amax);
+          p.scales[row * p.groups + (j + i * kTPR) / 16] = scale[i];
       }
     }
     uint8_t* o = static_cast<uint8_t*>(p.out) + row * W + j0;
 #pragma unroll
     for (int i = 0; i < kChunks; ++i) {
-      const float2 f = make_float2(factor[i], factor[i]);
+      // (over an infinite scale a number is 0 and an infinity has no value)
+      const float inv = rcp_approx(scale[i]), div = scale[i] < INFINITY ? -scale[i] : 0.f;
+      const auto quotient = [&](float2 v) {
+        const float2 f = make_float2(inv, inv), e = mul2<true>(v, f);
+        return fma2<true>(fma2<true>(e, make_float2(div, div), v), f, e);
+      };
       uint32_t q[2];
 #pragma unroll
       for (int h = 0; h < 2; ++h) {
-        const float2 a = mul2<true>(y[r][i][2 * h], f), b = mul2<true>(y[r][i][2 * h + 1], f);
+        const float2 a = quotient(y[r][i][2 * h]), b = quotient(y[r][i][2 * h + 1]);
         q[h] = e4m3x2(a.x, a.y) | (e4m3x2(b.x, b.y) << 16);
       }
       if constexpr (kStep == 8) {
