@@ -308,14 +308,22 @@ bool launch(NormParams p, cudaStream_t s) {
   const int W = p.width;
   if (W <= 128) p.group = 0;      // one scale group: the row
   if (W <= 64) return go<T, 8, 1, 128, 4>(p, s);
-  // Rows of 65 to 128: two chunks a thread, which spend less on addresses and sums than one, in
-  // 64 registers (393216 rows of 128 with gate in E4M3, us: 49.6; 51.5 without that limit; one
-  // chunk of four rows 55.9, of two 61).  Element by element one chunk is better (48000 rows of
-  // 125: 14.6 against 18.4).
+  // Rows of 65 to 128: two chunks a thread, which spend less on addresses and sums than one.  16-bit
+  // types: two rows of them in 64 registers (393216 rows of 128 BF16, us: with gate in E4M3 51.7,
+  // 53.8 without that limit, one chunk of two rows 64.0; the bare norm 37.4, 39.0, 44.1).  FP32 rows
+  // take twice the registers, and under that limit 436 bytes a thread went to memory and back: one
+  // row (294912 rows of 128, us, one row / two in 64 registers / two without a limit: bare 49.7 /
+  // 51.7 / 51.7, with residual and gate 114 / 175 / 115, gate in E4M3 53.8 / 71.5 / 57.8).  Element
+  // by element one chunk is better (48000 rows of 125: 14.6 against 18.4).
   if (W <= 128) {
-    if (p.step == 8) return go_step<T, 8, 2, 128, 2, 8, 8>(p, s);
-    if (p.step == 4) return go_step<T, 8, 2, 128, 2, 4, 8>(p, s);
-    return go_step<T, 16, 1, 128, 2, 1>(p, s);
+    if (p.step == 1) return go_step<T, 16, 1, 128, 2, 1>(p, s);
+    if constexpr (sizeof(typename T::Raw) == 4) {
+      if (p.step == 8) return go_step<T, 8, 2, 128, 1, 8>(p, s);
+      return go_step<T, 8, 2, 128, 1, 4>(p, s);
+    } else {
+      if (p.step == 8) return go_step<T, 8, 2, 128, 2, 8, 8>(p, s);
+      return go_step<T, 8, 2, 128, 2, 4, 8>(p, s);
+    }
   }
   if (W <= 256) return go<T, 32, 1, 128, 2>(p, s);
   if (W <= 512) return go<T, 32, 2, 128>(p, s);
@@ -324,6 +332,8 @@ bool launch(NormParams p, cudaStream_t s) {
   if (W <= 4096) return go<T, 256, 2, 256>(p, s);
   if (W <= 8192) return go<T, 256, 4, 256>(p, s);
   if (W <= 16384) return go<T, 512, 4, 512>(p, s);
+  // (FP32 rows leave 176 bytes a thread and more in memory here; 1024 threads of half as much have
+  // 64 registers and lose more: 1024 rows of 32768 89 against 121 us, with residual 122 against 177)
   return go<T, 512, 8, 512>(p, s);
 }
 
