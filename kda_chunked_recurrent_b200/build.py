@@ -1,15 +1,18 @@
 """Build the CUDA library libkda_prefill.so (nvcc, sm_100a only) and the Python binding of its
-layer operators, _layer_bind.so (g++, against torch), in-tree.
+layer operators, _layer_bind.so (g++, against torch), in-tree.  The library needs nvcc alone; the
+binding is left out, with a note, where torch, g++ or Python's headers are missing.
 
 Usage: python -m kda_chunked_recurrent_b200.build [--force] [--verbose]
 """
 from __future__ import annotations
 
 import argparse
+import importlib.util
 import os
 import shutil
 import subprocess
 import sys
+import sysconfig
 
 PKG = os.path.dirname(os.path.abspath(__file__))
 ROOT = os.path.dirname(PKG)
@@ -49,14 +52,20 @@ def _stale(target: str, inputs) -> bool:
     return any(os.path.getmtime(f) > t for f in inputs)
 
 
+def _missing_for_bind() -> list:
+    """What the binding's build needs and this machine lacks."""
+    header = os.path.join(sysconfig.get_paths()["include"], "Python.h")
+    return [what for what, found in (("torch", importlib.util.find_spec("torch")),
+                                     ("g++", shutil.which("g++")),
+                                     ("Python.h", os.path.exists(header))) if not found]
+
+
 def needs_build() -> bool:
-    return _stale(LIB, _inputs()) or _stale(BIND, _bind_inputs())
+    return _stale(LIB, _inputs()) or (_stale(BIND, _bind_inputs()) and not _missing_for_bind())
 
 
 def _bind_command(out: str) -> list:
     """g++ for the binding: torch's headers and libraries, the library beside it."""
-    import sysconfig
-
     import torch
     base = os.path.dirname(torch.__file__)
     cuda = os.path.dirname(os.path.dirname(nvcc_path()))
@@ -85,7 +94,11 @@ def build(force: bool = False, verbose: bool = False) -> str:
             print(" ".join(cmd), flush=True)
         subprocess.run(cmd, check=True)
         os.replace(tmp, LIB)
-    if force or _stale(BIND, _bind_inputs()):
+    missing = _missing_for_bind()
+    if missing:
+        print(f"{os.path.basename(BIND)} not built (the Python functions of the layer operators "
+              f"need it), missing: {', '.join(missing)}", file=sys.stderr, flush=True)
+    elif force or _stale(BIND, _bind_inputs()):
         tmp = BIND + f".tmp{os.getpid()}"
         cmd = _bind_command(tmp)
         if verbose:
