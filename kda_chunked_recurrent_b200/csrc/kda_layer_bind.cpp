@@ -13,6 +13,7 @@
 #include <torch/torch.h>
 
 #include <optional>
+#include <utility>
 
 #include "kda_layer.h"
 
@@ -59,8 +60,15 @@ int dtype_code(const Tensor& x) {
   }
   return -1;
 }
-void on_gpu(const Tensor& x) {
-  TORCH_CHECK_VALUE(x.is_cuda(), "x: a CUDA tensor expected, got one on ", x.device());
+// Asked last, when all else fits (so that the checks can be tested where there is no GPU), or
+// where a tensor lies elsewhere than x.
+void on_gpu(at::Device dev) {
+  TORCH_CHECK_VALUE(dev.is_cuda(), "x: a CUDA tensor expected, got one on ", dev);
+}
+bool same_device(const Tensor& t, at::Device dev) {
+  if (t.device() == dev) return true;
+  on_gpu(dev);
+  return false;
 }
 
 // A contiguous tensor of this type, shape and device: its address; NULL for none.
@@ -68,7 +76,7 @@ void* like(const Tensor* t, const char* name, at::ScalarType type, at::IntArrayR
            at::Device dev) {
   if (t == nullptr) return nullptr;
   TORCH_CHECK_VALUE(t->scalar_type() == type && t->sizes() == shape && t->is_contiguous() &&
-                        t->device() == dev,
+                        same_device(*t, dev),
                     name, ": a contiguous ", type, " tensor of shape ", shape, " on ", dev,
                     " expected, got ", t->scalar_type(), " ", t->sizes(), " on ", t->device(),
                     ", strides ", t->strides());
@@ -79,7 +87,7 @@ void* values(const Tensor* t, const char* name, at::ScalarType a, at::ScalarType
              at::Device dev) {
   if (t == nullptr) return nullptr;
   TORCH_CHECK_VALUE((t->scalar_type() == a || t->scalar_type() == b) && t->numel() == n &&
-                        t->is_contiguous() && t->device() == dev,
+                        t->is_contiguous() && same_device(*t, dev),
                     name, ": ", n, " contiguous ", a, " values on ", dev, " expected, got ",
                     t->numel(), " of ", t->scalar_type(), " on ", t->device());
   return t->data_ptr();
@@ -88,7 +96,7 @@ void* values(const Tensor* t, const char* name, at::ScalarType a, at::ScalarType
 // contiguous row and whose leading dimensions step through rows at one distance.
 int64_t rows(const Tensor& t, const char* name, at::ScalarType type, at::IntArrayRef shape,
              at::Device dev, int tail = 1) {
-  TORCH_CHECK_VALUE(t.scalar_type() == type && t.sizes() == shape && t.device() == dev, name,
+  TORCH_CHECK_VALUE(t.scalar_type() == type && t.sizes() == shape && same_device(t, dev), name,
                     ": a ", type, " tensor of shape ", shape, " on ", dev, " expected, got ",
                     t.scalar_type(), " ", t.sizes(), " on ", t.device());
   const auto st = t.strides();
@@ -110,13 +118,26 @@ int64_t rows(const Tensor& t, const char* name, at::ScalarType type, at::IntArra
   TORCH_CHECK_VALUE(row >= n, name, ": rows must not overlap, strides ", st);
   return row;
 }
-// The caller's output, checked, or a new one.
-Tensor output(const Tensor* given, const char* name, at::ScalarType type, at::IntArrayRef shape,
-              const Tensor& x) {
-  if (given == nullptr) return at::empty(shape, x.options().dtype(type));
-  like(given, name, type, shape, x.device());
-  return *given;
-}
+// An output: the caller's, checked, or a new one, allocated when the call is made.
+class Output {
+ public:
+  Output(PyObject* given, const char* name, at::ScalarType type, Shape shape, const Tensor& x)
+      : type_(type), shape_(std::move(shape)) {
+    const Tensor* t = tensor(given, name);
+    if (t == nullptr) return;
+    like(t, name, type, shape_, x.device());
+    given_ = *t;
+  }
+  bool given() const { return given_.has_value(); }
+  Tensor make(const Tensor& x) const {
+    return given_ ? *given_ : at::empty(shape_, x.options().dtype(type_));
+  }
+
+ private:
+  at::ScalarType type_;
+  Shape shape_;
+  std::optional<Tensor> given_;
+};
 
 struct Seqs {
   int64_t num;
@@ -148,12 +169,12 @@ Seqs seqs(int64_t n_rows, PyObject* cu_o, PyObject* num_o, const Tensor* state, 
   return s;
 }
 
-// ---- the call: on the tensors' device, its current stream unless one is given.  Made before
-// the outputs: they are then allocated on the stream that writes them, as under
+// ---- the call: on the tensors' device, its current stream unless one is given.  Made behind the
+// checks and before the outputs: they are then allocated on the stream that writes them, as under
 // torch.cuda.stream(); memory of another stream may still be in use there.
 class Call {
  public:
-  Call(at::Device dev, PyObject* stream) : device_(dev) {
+  Call(at::Device dev, PyObject* stream) : device_((on_gpu(dev), dev)) {
     if (stream == Py_None) {
       stream_ = c10::cuda::getCurrentCUDAStream(dev.index()).stream();
       return;
@@ -251,13 +272,13 @@ PyObject* conv_prefill(PyObject*, PyObject* const* a, Py_ssize_t nargs) {
   KDA_ARGS(13)
   const Tensor& x = need(a[0], "x");
   TORCH_CHECK_VALUE(x.dim() == 2, "x: [T, C] expected");
-  on_gpu(x);
-  const Call call(x.device(), a[12]);
   const Tensor* state = tensor(a[3], "state");
   const Conv c = conv_args(x, a[1], a[2], state, a[8]);
   const Seqs s = seqs(x.size(0), a[6], a[7], state, a[4], a[5], a[11], x.device());
   const kda_conv_shape_t shape = conv_shape(c, s.num, x.size(0), x);
-  const Tensor out = output(tensor(a[10], "out"), "out", x.scalar_type(), c.out, x);
+  const Output output(a[10], "out", x.scalar_type(), c.out, x);
+  const Call call(x.device(), a[12]);
+  const Tensor out = output.make(x);
   const uint32_t flags = s.flags | (truth(a[9]) ? KDA_CONV_SILU : 0u);
   call.launch("kda_conv_prefill", [&](void* stream) {
     return kda_conv_prefill(x.data_ptr(), as<float>(c.weight), as<float>(c.bias), c.state,
@@ -275,8 +296,6 @@ PyObject* conv_decode(PyObject*, PyObject* const* a, Py_ssize_t nargs) {
   KDA_ARGS(13)
   const Tensor& x = need(a[0], "x");
   TORCH_CHECK_VALUE(x.dim() == 3, "x: [N, T, C] expected");
-  on_gpu(x);
-  const Call call(x.device(), a[12]);
   const at::Device dev = x.device();
   const int64_t N = x.size(0), T = x.size(1);
   const Tensor& state = need(a[3], "state");
@@ -284,11 +303,12 @@ PyObject* conv_decode(PyObject*, PyObject* const* a, Py_ssize_t nargs) {
   const kda_conv_shape_t shape = conv_shape(c, N, T, x);
   void* slots = values(tensor(a[4], "state_indices"), "state_indices", at::kInt, at::kInt, N, dev);
   void* status = values(tensor(a[11], "device_status"), "device_status", at::kInt, at::kInt, 1, dev);
-  const Tensor out = output(tensor(a[7], "out"), "out", x.scalar_type(), c.out, x);
+  const Output output(a[7], "out", x.scalar_type(), c.out, x);
+  const Output step_output(a[8], "step_states", x.scalar_type(), {N, T, c.width - 1, c.ch}, x);
+  const Call call(dev, a[12]);
+  const Tensor out = output.make(x);
   std::optional<Tensor> steps;
-  const Tensor* steps_in = tensor(a[8], "step_states");
-  if (steps_in != nullptr || truth(a[9]))
-    steps = output(steps_in, "step_states", x.scalar_type(), {N, T, c.width - 1, c.ch}, x);
+  if (step_output.given() || truth(a[9])) steps = step_output.make(x);
   const uint32_t flags =
       (truth(a[6]) ? KDA_CONV_SILU : 0u) | (truth(a[10]) ? KDA_LAYER_KEEP_STATE : 0u);
   call.launch("kda_conv_decode", [&](void* stream) {
@@ -356,15 +376,15 @@ PyObject* scan_prefill(PyObject*, PyObject* const* a, Py_ssize_t nargs) {
   KDA_ARGS(18)
   const Tensor& x = need(a[0], "x");
   TORCH_CHECK_VALUE(x.dim() == 2, "x: [T, D] expected");
-  on_gpu(x);
-  const Call call(x.device(), a[17]);
   Scan c = scan_args(a);
   const Seqs s = seqs(x.size(0), a[11], a[12], tensor(a[8], "state"), a[9], a[10], a[16],
                       x.device());
   c.shape.num_seqs = int32(s.num, "sequences");
   c.shape.tokens = int32(x.size(0), "tokens");
   c.shape.max_seqlen = int32(integer(a[13]), "max_seqlen");
-  const Tensor out = output(tensor(a[15], "out"), "out", x.scalar_type(), x.sizes(), x);
+  const Output output(a[15], "out", x.scalar_type(), Shape(x.sizes()), x);
+  const Call call(x.device(), a[17]);
+  const Tensor out = output.make(x);
   const uint32_t flags = s.flags | (truth(a[14]) ? KDA_SCAN_SOFTPLUS : 0u);
   call.launch("kda_scan_prefill", [&](void* stream) {
     return kda_scan_prefill(c.x, c.dt, as<float>(c.A_log), c.B, c.C, as<float>(c.D), c.z,
@@ -383,8 +403,6 @@ PyObject* scan_decode(PyObject*, PyObject* const* a, Py_ssize_t nargs) {
   KDA_ARGS(17)
   const Tensor& x = need(a[0], "x");
   TORCH_CHECK_VALUE(x.dim() == 3, "x: [N, T, D] expected");
-  on_gpu(x);
-  const Call call(x.device(), a[16]);
   need(a[8], "state");
   const at::Device dev = x.device();
   const int64_t N = x.size(0), T = x.size(1);
@@ -393,12 +411,13 @@ PyObject* scan_decode(PyObject*, PyObject* const* a, Py_ssize_t nargs) {
   c.shape.tokens = int32(T, "tokens");
   void* slots = values(tensor(a[9], "state_indices"), "state_indices", at::kInt, at::kInt, N, dev);
   void* status = values(tensor(a[15], "device_status"), "device_status", at::kInt, at::kInt, 1, dev);
-  const Tensor out = output(tensor(a[11], "out"), "out", x.scalar_type(), x.sizes(), x);
+  const Output output(a[11], "out", x.scalar_type(), Shape(x.sizes()), x);
+  const Output step_output(a[12], "step_states", at::kFloat,
+                           {N, T, x.size(2), static_cast<int64_t>(c.shape.state_size)}, x);
+  const Call call(dev, a[16]);
+  const Tensor out = output.make(x);
   std::optional<Tensor> steps;
-  const Tensor* steps_in = tensor(a[12], "step_states");
-  if (steps_in != nullptr || truth(a[13]))
-    steps = output(steps_in, "step_states", at::kFloat,
-                   {N, T, x.size(2), static_cast<int64_t>(c.shape.state_size)}, x);
+  if (step_output.given() || truth(a[13])) steps = step_output.make(x);
   const uint32_t flags =
       (truth(a[10]) ? KDA_SCAN_SOFTPLUS : 0u) | (truth(a[14]) ? KDA_LAYER_KEEP_STATE : 0u);
   call.launch("kda_scan_decode", [&](void* stream) {
@@ -419,8 +438,6 @@ PyObject* rms_norm(PyObject*, PyObject* const* a, Py_ssize_t nargs) {
   const Tensor& x = need(a[0], "x");
   const int dims = static_cast<int>(x.dim()), tail = dims - 1;
   TORCH_CHECK_VALUE(dims == 2 || dims == 3, "x: [T, W] or [T, H, W] expected");
-  on_gpu(x);
-  const Call call(x.device(), a[11]);
   const at::Device dev = x.device();
   const at::ScalarType type = x.scalar_type();
   const Tensor *res = tensor(a[3], "residual"), *gate = tensor(a[4], "gate"),
@@ -444,17 +461,19 @@ PyObject* rms_norm(PyObject*, PyObject* const* a, Py_ssize_t nargs) {
   if (res != nullptr) sh.residual_stride = rows(*res, "residual", type, x.sizes(), dev, tail);
   if (gate != nullptr) sh.gate_stride = rows(*gate, "gate", type, x.sizes(), dev, tail);
   void* weight = like(tensor(a[1], "weight"), "weight", at::kFloat, {W}, dev);
-  const Tensor out = output(tensor(a[8], "out"), "out", bits8 ? at::kFloat8_e4m3fn : type,
-                            x.sizes(), x);
+  const Output output(a[8], "out", bits8 ? at::kFloat8_e4m3fn : type, Shape(x.sizes()), x);
+  sh.residual_out_stride =
+      res_out_in != nullptr ? rows(*res_out_in, "residual_out", type, x.sizes(), dev, tail)
+                            : sh.heads * W;
+  Shape per_row(x.sizes().begin(), x.sizes().end() - 1);
+  per_row.push_back(group == 0 ? 1 : (W + 127) / 128);
+  const Output scale_output(a[10], "scales", at::kFloat, per_row, x);
+  const Call call(dev, a[11]);
+  const Tensor out = output.make(x);
   std::optional<Tensor> res_out, scales;
   if (res_out_in != nullptr) res_out = *res_out_in;
   else if (res != nullptr) res_out = at::empty(x.sizes(), x.options());
-  if (res_out) sh.residual_out_stride = rows(*res_out, "residual_out", type, x.sizes(), dev, tail);
-  if (bits8) {
-    Shape s(x.sizes().begin(), x.sizes().end() - 1);
-    s.push_back(group == 0 ? 1 : (W + 127) / 128);
-    scales = output(scales_in, "scales", at::kFloat, s, x);
-  }
+  if (bits8) scales = scale_output.make(x);
   const uint32_t flags = static_cast<uint32_t>(integer(a[5]));
   call.launch("kda_rms_norm", [&](void* stream) {
     return kda_rms_norm(x.data_ptr(), as<float>(weight), res ? res->data_ptr() : nullptr,
