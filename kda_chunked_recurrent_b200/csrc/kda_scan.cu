@@ -907,19 +907,31 @@ bool go_prefill(ScanParams p, int sms, cudaStream_t s) {
 }
 
 // Few channels and many rows: the rows are shared by a cluster of 8 or 4 CTAs.  A run is taken
-// twice, so the time falls to a quarter or a half at best.  One sequence, 16-bit rows, us, by
-// one CTA / 4 / 8 (256 channels; 592; 1024):
-//    512 rows   16.5 / 12.4 / 12.3;   16.5 / 16.0 / 18.9
-//   2048 rows   52.6 / 30.9 / 24.8;   55.4 / 43.2 / 44.2
-//   4096 rows    100 / 53.6 / 43.2;                         109 / 83 / 89
-// and more channels than that fill the SMs without.
+// twice, so the time falls to a quarter or a half at best.  Up to 16 elements several CTAs share an
+// SM and the clusters may hold twice the SMs; the wider layouts fill an SM's shared memory, and
+// clusters that wait for a place cost more than they bring (33 clusters of 4 find one at a time, and
+// 9 of 8 or some more).  One sequence, 16-bit rows, us, by one CTA / 4 / 8:
+//                              512 rows             4096 rows
+//   16 elements,  256 ch   16.6 / 12.5 / 12.5    103 / 53.5 / 43.3
+//                 512      16.6 / 12.5 / 12.5    103 / 55.5 / 45.3
+//                1024      16.6 / 16.6 / 21.0    104 / 81.4 / 87.0
+//   64 elements,  128      33.0 / 24.8 / 24.8    230 /  117 / 71.9
+//                 512      33.0 / 25.1 / 45.1    230 /  119 /  136
+//                1024      34.6 / 38.9 / 81.7    232 /  236 /  271
+//  128 elements,   64      49.4 / 31.0 / 26.6    359 /  174 / 98.5
+//                 256      49.3 / 30.9 / 70.3    359 /  175 /  282
+//                 512      49.4 / 57.6 /  114    357 /  343 /  469
+// and more channels than that fill the SMs without.  FP32 rows turn at the same places.
 template <typename T, typename C>
 bool pick_prefill(const ScanParams& p, int64_t max_rows, int sms, cudaStream_t s) {
   const int64_t tiles = static_cast<int64_t>(p.seq.num) * p.groups *
                         ((p.per_group + C::kCH - 1) / C::kCH);
+  constexpr bool kWide = C::kNP > 16;
   if (max_rows >= 512) {
-    if (tiles * 32 <= 7LL * sms) return go_prefill<T, C, 8>(p, sms, s);
-    if (tiles * 4 <= 2LL * sms) return go_prefill<T, C, 4>(p, sms, s);
+    const bool eight = kWide ? tiles * 16 <= sms : tiles * 32 <= 7LL * sms;
+    const bool four = kWide ? tiles * 9 <= 2LL * sms : tiles * 4 <= 2LL * sms;
+    if (eight) return go_prefill<T, C, 8>(p, sms, s);
+    if (four) return go_prefill<T, C, 4>(p, sms, s);
   }
   return go_prefill<T, C, 1>(p, sms, s);
 }
@@ -961,11 +973,20 @@ bool launch_tokens(const ScanParams& p, bool prompts, int sms, cudaStream_t s) {
 
 template <typename T>
 bool launch_prefill(const ScanParams& p, int64_t max_rows, int sms, cudaStream_t s) {
-  // Many sequences of few rows: row by row in the token kernel.  A block of the kernel above
-  // costs a CTA about 5 us however few rows it has.  32 sequences of 1 / 4 / 16 / 32 rows of
-  // 2048 channels, us, token kernel and this: 6.3 / 10.2 / 20.6 / 37 and 22.7 / 22.7 / 27 / 33.
+  // Many sequences of few rows: row by row in the token kernel.  A block of the kernel above costs a
+  // CTA about 5 us however few rows it has (above 64 elements, one CTA an SM, 25).  us, token
+  // kernel / this one, 16-bit rows:
+  //                                        8 rows        16           24           32
+  //   16 elements, 32 x 2048 channels   14.6 / 24.8  21.0 / 28.9  28.9 / 31.7  36.6 / 33.3
+  //                13 x 2520            13.6 / 14.6  20.7 / 16.6  28.9 / 18.7  35.1 / 19.4
+  //                64 x 512             11.3 / 16.6  16.5 / 18.7  22.8 / 19.4  27.1 / 20.7
+  //   64 elements, 32 x 2048            41.2 / 66.8  69.6 / 74.0  96.8 / 82.4   130 / 92.5
+  //                13 x 2520            29.4 / 33.8  49.2 / 37.4  67.8 / 43.2  86.3 / 47.6
+  //  128 elements, 32 x 2048            81.9 /  218   148 /  244   216 /  266   283 /  301
+  //                13 x 2520            50.2 /  111  85.8 /  123   120 /  133   155 /  149
+  // (at 16 rows of up to 64 elements either may win: even over ten such batches and two types)
   const int64_t ctas = static_cast<int64_t>(p.seq.num) * p.channels / 32;
-  if (max_rows <= 16 && ctas > 2LL * sms) return launch_tokens<T>(p, true, sms, s);
+  if (max_rows <= (p.size > 64 ? 28 : 16) && ctas > 2LL * sms) return launch_tokens<T>(p, true, sms, s);
   if (p.size > 64) return pick_prefill<T, Cfg<T, 128, 8>>(p, max_rows, sms, s);
   if (p.size > 32) return pick_prefill<T, Cfg<T, 64, 8>>(p, max_rows, sms, s);
   if (p.size > 16) return pick_prefill<T, Cfg<T, 32, 4>>(p, max_rows, sms, s);
