@@ -28,7 +28,8 @@
  * Counts of rows, of sequences and of a token's elements end at 2^31 - 4097.
  *
  * Not finite values: an infinity or a NaN stays in the windows, the channel's states or the
- * row that it is in; the SiLU of minus infinity is a NaN.
+ * row that it is in, and leaves the rows before it as they are; the SiLU of minus infinity is a
+ * NaN, and so may be a sum of the scan that has an infinity in it.
  */
 #ifndef KDA_LAYER_H_
 #define KDA_LAYER_H_

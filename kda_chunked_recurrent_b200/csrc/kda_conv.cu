@@ -6,8 +6,10 @@
 // Every channel is on its own and every input row is needed by W outputs, so the work is a
 // copy with a little arithmetic: 2 bytes in, 2 bytes out, W FMAs and (SiLU) two special
 // functions per element.  Bound: HBM, with the special functions not far behind (29K rows of
-// 4608 BF16 channels: 81 us of bytes, 58 us of special functions; 97 us measured, 5.5
-// TB/s).
+// 4608 BF16 channels: 81 us of bytes, 58 us of special functions; 102 us measured, 5.2
+// TB/s).  That and the figure for tokens are of passes among others, each over inputs that no pass
+// just before used; where two forms are compared below, of calls back to back over three sets of
+// inputs, which read some 5% less.
 //
 // Prompts.  A thread owns kV adjacent channels and walks strips of kStrip rows: all rows
 // of a strip are loaded at once, a strip ahead (these loads are what keeps HBM busy), the
@@ -18,7 +20,7 @@
 // and nobody else touches them, the update in place needs no further ordering.
 //
 // Tokens.  One thread per kV channels of a sequence: state rows and new rows in, outputs
-// and the shifted state out (1024 sequences of 4608 BF16 channels 16.5 us, 4.6 TB/s).
+// and the shifted state out (1024 sequences of 4608 BF16 channels 16.9 us, 4.5 TB/s).
 #include <algorithm>
 
 #include "kda_layer.cuh"
@@ -62,7 +64,7 @@ struct Taps {
       for (int j = 0; j < W; ++j) a = fmaf(w[j][0], u[j][0], a);
       y[0] = act ? a * sigmoid(a) : a;
     } else {
-float2 a[kV / 2];
+      float2 a[kV / 2];
 #pragma unroll
       for (int i = 0; i < kV / 2; ++i) {
         a[i] = make_float2(bias[2 * i], bias[2 * i + 1]);

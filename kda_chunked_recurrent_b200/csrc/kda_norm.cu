@@ -8,9 +8,11 @@
 // sums; nothing else is to be done, so the bound is HBM for many rows and the latency of
 // one load, two reductions and one store for few.  r is not rounded before the norm (the
 // stored residual is its rounding): one rounding fewer than norming the stored sum.
-// 8192 rows of 4096 BF16 with residual: 43.4 us, 6.2 TB/s; 393216 rows of 128 with gate, in
-// E4M3: 49.6 us, 5.1 TB/s, there bound by issued instructions, two special functions an element
-// for the gate among them.
+// 8192 rows of 4096 BF16 with residual: 43.8 us, 6.1 TB/s; 393216 rows of 128 with gate, in
+// E4M3: 55.3 us, 4.6 TB/s, there bound by issued instructions, two special functions an element
+// for the gate among them.  (Passes among others, each over inputs that no pass just before used;
+// where two forms are compared below, calls back to back over two or three sets of inputs, which
+// read up to 7% less.)
 //
 // kTPR threads share a row: a part of a warp for short rows (the heads of a token: no
 // barrier at all), several warps for long ones (one barrier per reduction).  A thread holds

@@ -6,7 +6,7 @@
 //
 // Every state element is a recurrence of its own: one exponential, three products and a sum
 // per row, and a sum over the elements of a channel.  With 16 elements a channel and 16-bit
-// rows that is 16 exponentials (and 3.5 more special functions for softplus and gate) for 8
+// rows that is 16 exponentials (and 4 more special functions for softplus and gate) for 8
 // bytes, and an SM makes 16 a clock, so prompts are bound by the special-function units, at
 // about 2 TB/s of row bytes, not by HBM; single tokens, which move 8 bytes of state per
 // exponential, by HBM.
@@ -19,18 +19,18 @@
 // and d x once per (row, channel) one block ahead, and, one block behind, add the lanes' parts
 // of the sums and write the output rows (skip, gate, rounding).  One barrier a block.
 //
-// Measured: 8192 rows of 4096 BF16 channels 285 us, of which the exponentials alone would
-// take 150 at their rate, all special functions 171 (128 of 148 SMs have work); 16 ragged
-// prompts of 2048 FP16 channels 365 us, against 260.  With one scan and one helper warp on a
-// scheduler the rest is latency: a row takes 67 clocks, where the scan warp's 4
-// exponentials a lane need 32 and the helpers' special functions 5.  Tried and dropped, us
-// for the first: one exponential in eight on the FMA pipe 337 (of 312 then), B and C in FP32
-// and d in pairs in shared memory 306 (of 285; in pairs alone 294), separate warps for staging
-// and writing 283 (of 293), but 386 of 373 for the ragged prompts, two channels per lane 419
-// (of 401, ragged).
+// Measured (passes among others, each over inputs that no pass just before used): 8192 rows of
+// 4096 BF16 channels 287 us.  At 16 a clock and SM and 1.92 GHz the exponentials alone take 137 on
+// the 128 SMs that have work, all special functions, 20 a row and channel, 171 (148 on all 148).  16
+// ragged prompts of 2048 FP16 channels 362 us, against 259.  With one scan and one helper warp on a
+// scheduler the rest is latency: a row takes 67 clocks, where the scan warp's 4 exponentials a lane
+// need 32 and the helpers' special functions 8.  Tried and dropped, us for the first, each beside
+// the form of its time: one exponential in eight on the FMA pipe 337 (of 312), B and C in FP32 and d
+// in pairs in shared memory 306 (of 285; in pairs alone 294), separate warps for staging and writing
+// 283 (of 293), but 386 of 373 for the ragged prompts, two channels per lane 419 (of 401, ragged).
 //
 // Tokens.  Four state elements (16 bytes) per thread, the state read and written once; four
-// sequences at a time.  256 sequences of 4096 channels 32.9 us, 4.3 TB/s.
+// sequences at a time.  256 sequences of 4096 channels 33.5 us, 4.3 TB/s.
 #include <algorithm>
 #include <type_traits>
 
