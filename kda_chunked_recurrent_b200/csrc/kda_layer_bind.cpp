@@ -193,7 +193,10 @@ class Call {
 };
 template <typename F>
 void Call::launch(const char* where, F&& call) const {
+  // Other Python threads run meanwhile: a launch into a full queue waits until there is room.
+  PyThreadState* const thread = PyEval_SaveThread();
   const kda_status_t rc = call(static_cast<void*>(stream_));
+  PyEval_RestoreThread(thread);
   if (rc == KDA_OK) return;
   PyObject* r = PyObject_CallFunction(g_fail, "is", static_cast<int>(rc), where);
   Py_XDECREF(r);
