@@ -219,3 +219,22 @@ def test_shared_rows_keep_an_infinite_state():
     pool[0, 4, 7] = INF
     K.scan_prefill(x, dt, torch.zeros(D, S, device="cuda"), B, C, state=pool, softplus=False)
     assert pool[0, 4, 7] == INF and torch.isfinite(pool).sum() == D * S - 1
+
+
+@pytest.mark.parametrize("N,T,D,S,G", [(5, 7, 96, 13, 3), (3, 4, 65, 16, 1), (2, 6, 40, 128, 2)])
+def test_tokens_bounded_negative_steps(N, T, D, S, G):
+    """Steps of both signs that leave the states at a usual size, so that every value is asked for."""
+    g = torch.Generator().manual_seed(N)
+    r = lambda *s: torch.randn(*s, generator=g)  # noqa: E731
+    x, z, B, C = r(N, T, D).cuda(), r(N, T, D).cuda(), r(N, T, G, S).cuda(), r(N, T, G, S).cuda()
+    dt, A_log, pool = (0.05 * r(N, T, D)).cuda(), torch.log(1 + torch.rand(D, S, generator=g) * 9).cuda(), \
+        r(N, D, S).cuda()
+    before = f64(pool)
+    out, steps = K.scan_decode(x, dt, A_log, B, C, pool, z=z, softplus=False, return_step_states=True)
+    for n in range(N):
+        y, yb, hs, es = scan(f64(x[n]), f64(dt[n]), f64(A_log), f64(B[n]), f64(C[n]), None, f64(z[n]),
+                             None, before[n], False)
+        assert np.abs(hs).max() < 2.0 ** 40
+        close(out[n], y, yb, torch.float32, f"rows of sequence {n}")
+        close(steps[n], hs, es, torch.float32, f"step states of sequence {n}")
+        close(pool[n], hs[-1], es[-1], torch.float32, f"state of sequence {n}")
